@@ -28,12 +28,14 @@ EXPORTS = ["moe_packed_size", "moe_pack_experts", "moe_requantize_q3_to_q2", "mo
            "moe_forward", "moe_forward_timed", "moe_get_error", "moe_decode_static", "moe_decode_static_get_error",
            "moe_workspace_set_test_stall", "moe_event_record", "moe_status_string", "moe_abi_version",
            "moe_route_fixed", "moe_gather_rows", "moe_combine_pairs", "moe_cache_size", "moe_cache_init",
-           "moe_cache_load", "moe_forward_plan"]
+           "moe_cache_load", "moe_forward_plan", "moe_linear"]
 # detail codes beside MOE_ERR_TIMEOUT / MOE_ERR_DEVICE_CHECK (high bits: what; low byte: where)
 DETAIL = {"WAIT_FULL": 0x100, "WAIT_EMPTY": 0x200, "DRAIN": 0x300, "HEADER": 0x400, "ROUTED_T": 0x500,
           "RANGE": 0x600, "TEST_STALL": 0x700, "LOOP_CAP": 0x800, "FORMAT": 0x900}
 FMT_TERNARY_DENSE = 3       # storage form of ternary experts (five codes per byte), see moe.h
 STATIC_WS_BYTES = 8 << 20
+BF16, F16, F32 = 0, 1, 2                                                   # moe_dtype
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = range(6)   # moe_act
 
 
 class MoeError(RuntimeError):
@@ -53,6 +55,12 @@ class Routing(ctypes.Structure):
 
 class MatrixSrc(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("hi", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("act", ctypes.c_int), ("ldx", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 _lib = None
@@ -87,6 +95,7 @@ def lib() -> ctypes.CDLL:
         L.moe_cache_size.argtypes = [sh, vp, i32, ctypes.POINTER(sz)]
         L.moe_cache_init.argtypes = [sh, vp, i32, vp, sz, vp]
         L.moe_cache_load.argtypes = [sh, vp, i32, vp, sz, vp, vp, i32, vp]
+        L.moe_linear.argtypes = [ctypes.POINTER(LinearDesc), i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_event_record.argtypes = [vp, vp]
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -115,6 +124,15 @@ def _stream(stream=None):
     import torch
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _on(device):
+    """Context with `device` current (nothing to do when it already is)."""
+    import contextlib
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 # ---- packing (host) -----------------------------------------------------------
@@ -291,6 +309,59 @@ def moe_combine_pairs(T, k, rows, inv_perm, gates, shared, y, ws, stream=None) -
     _check("moe_combine_pairs", lib().moe_combine_pairs(T, k, y.shape[1], _ptr(rows), rows.shape[0], _ptr(inv_perm),
                                                          _ptr(gates), _ptr(shared), _ptr(y), _ptr(ws),
                                                          ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _rows(name, t, shape, dtypes, device):
+    """Row stride of a matrix argument; raises ValueError unless it is a tensor of this
+    shape, one of these types, on this device, with adjacent elements in a row."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
+        raise ValueError(f"{name}: expected {shape} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} on "
+                         f"{t.device}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent, got strides {t.stride()}")
+    return t.stride(0)
+
+
+def moe_linear(x, w, y, ws, bias=None, residual=None, act=ACT_NONE, stream=None) -> None:
+    """y = act(x w^T + bias) + residual for bfloat16 or float16 x [T][K], w [N][K] and y [T][N]
+    (ACT_SWIGLU: w [2N][K], the gate rows first, and y = silu(gate) * up + residual).
+    residual: [T][N] of x's type or float32; y itself for an update in place.  Rows may be
+    strided (x, w: strides that are multiples of 8 elements).  ws: any initialised workspace
+    (its control block records device errors).  Runs on `stream` (default: the current stream
+    of x's device)."""
+    import torch
+    dt, dev = x.dtype, x.device
+    if dt not in (torch.bfloat16, torch.float16) or x.dim() != 2 or w.dim() != 2:
+        raise ValueError("moe_linear: x and w must be bfloat16 or float16 matrices")
+    if not x.is_cuda or ws.device != dev:
+        raise ValueError("moe_linear: x and ws must be on one CUDA device")
+    T, K = x.shape
+    n_w = w.shape[0]
+    N = n_w // 2 if act == ACT_SWIGLU else n_w
+    if act == ACT_SWIGLU and n_w != 2 * N:
+        raise ValueError("moe_linear: ACT_SWIGLU needs an even number of weight rows")
+    # a row stride means nothing to a single row: any valid one will do
+    up = (max(K, 1) + 7) // 8 * 8
+    ldx = _rows("x", x, (T, K), (dt,), dev) if T > 1 else (_rows("x", x, (T, K), (dt,), dev), up)[1]
+    ldw = _rows("w", w, (n_w, K), (dt,), dev) if n_w > 1 else (_rows("w", w, (n_w, K), (dt,), dev), up)[1]
+    ldy = _rows("y", y, (T, N), (dt,), dev)
+    ldy = ldy if T > 1 else N
+    ldr, rt = 0, F32
+    if residual is not None:
+        ldr = _rows("residual", residual, (T, N), (dt, torch.float32), dev)
+        ldr = ldr if T > 1 else N
+        rt = F32 if residual.dtype == torch.float32 else (BF16 if dt == torch.bfloat16 else F16)
+    if bias is not None and (tuple(bias.shape) != (n_w,) or bias.dtype != dt or bias.device != dev
+                             or (n_w > 1 and bias.stride(0) != 1)):
+        raise ValueError(f"bias: expected ({n_w},) contiguous of {dt} on {dev}")
+    d = LinearDesc(K, N, BF16 if dt == torch.bfloat16 else F16, rt, act, ldx, ldw, ldr, ldy)
+    with _on(dev):
+        s = stream if stream is not None else torch.cuda.current_stream(dev)
+        st = lib().moe_linear(ctypes.byref(d), T, x.data_ptr(), w.data_ptr(),
+                              None if bias is None else bias.data_ptr(),
+                              None if residual is None else residual.data_ptr(), y.data_ptr(), ws.data_ptr(),
+                              ws.numel() * ws.element_size(), s.cuda_stream)
+    _check("moe_linear", st)
 
 
 def moe_get_error(ws, stream=None):

@@ -165,6 +165,17 @@ moe_status plan_forward(const moe_shape* shape, int64_t T, moe_path path, Forwar
     return MOE_OK;
 }
 
+// Whether two strided matrices (base, rows, bytes of a row, row stride in bytes) share
+// memory.  Column slices of one buffer have one stride and interleave without sharing.
+bool overlap(const void* pa, int64_t ra, int64_t wa, int64_t la, const void* pb, int64_t rb, int64_t wb, int64_t lb) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
+    const uintptr_t ea = a + (uintptr_t)((ra - 1) * la + wa), eb = b + (uintptr_t)((rb - 1) * lb + wb);
+    if (a >= eb || b >= ea) return false;
+    if (la != lb || ra <= 1 || rb <= 1) return true;
+    const int64_t d = b >= a ? (int64_t)((b - a) % (uintptr_t)la) : (la - (int64_t)((a - b) % (uintptr_t)la)) % la;
+    return d < wa || d + wb > la;
+}
+
 // Writes the test-stall word of a workspace's control block (one thread).
 __global__ void set_test_stall_kernel(Ctrl* c, uint32_t cycles) { c->test_stall = cycles; }
 
@@ -300,6 +311,56 @@ moe_status moe_combine_pairs(int32_t T, int32_t top_k, int32_t hidden, const flo
                                 static_cast<Ctrl*>(d_ws), static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
+}
+
+moe_status moe_linear(const moe_linear_desc* desc, int32_t T, const void* d_x, const void* d_w, const void* d_bias,
+                      const void* d_residual, void* d_y, void* d_ws, size_t ws_bytes, void* stream) {
+    if (!desc || T < 0 || desc->in_features < 1 || desc->out_features < 1) return MOE_ERR_INVALID_ARG;
+    const moe_linear_desc& d = *desc;
+    if (d.dtype != MOE_BF16 && d.dtype != MOE_F16) return MOE_ERR_INVALID_ARG;
+    if ((int)d.act < MOE_ACT_NONE || (int)d.act > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+    const int64_t K = d.in_features, N = d.out_features, wrows = d.act == MOE_ACT_SWIGLU ? 2 * N : N;
+    // a row stride of the maps is at most 2^40 bytes
+    const int64_t max_ld = (int64_t)1 << 38;
+    if (d.ldx < K || d.ldw < K || d.ldy < N || d.ldx % 8 || d.ldw % 8) return MOE_ERR_INVALID_ARG;
+    if (d.ldx > max_ld || d.ldw > max_ld || d.ldy > max_ld) return MOE_ERR_INVALID_ARG;
+    const bool res_f32 = d.residual_dtype == MOE_F32;
+    if (d_residual && ((!res_f32 && d.residual_dtype != d.dtype) || d.ldr < N || d.ldr > max_ld))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!d_x || !d_w || !d_y || !d_ws || ws_bytes < 4096) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(d_x) || !aligned16(d_w) || !aligned16(d_ws)) return MOE_ERR_INVALID_ARG;
+    const uintptr_t odd = reinterpret_cast<uintptr_t>(d_y) | reinterpret_cast<uintptr_t>(d_bias);
+    const uintptr_t rodd = reinterpret_cast<uintptr_t>(d_residual);
+    if ((odd & 1) || (rodd & (res_f32 ? 3 : 1))) return MOE_ERR_INVALID_ARG;
+    const int64_t rsize = res_f32 ? 4 : 2;
+    if (overlap(d_y, T, 2 * N, 2 * d.ldy, d_x, T, 2 * K, 2 * d.ldx) ||
+        overlap(d_y, T, 2 * N, 2 * d.ldy, d_w, wrows, 2 * K, 2 * d.ldw) ||
+        (d_bias && overlap(d_y, T, 2 * N, 2 * d.ldy, d_bias, 1, 2 * wrows, 2 * wrows)))
+        return MOE_ERR_INVALID_ARG;
+    const bool in_place = d_residual == d_y && !res_f32 && (d.ldr == d.ldy || T == 1);
+    if (d_residual && !in_place && overlap(d_y, T, 2 * N, 2 * d.ldy, d_residual, T, rsize * N, rsize * d.ldr))
+        return MOE_ERR_INVALID_ARG;
+    if (wrows > INT32_MAX - 256 || T > INT32_MAX - 256 || K > INT32_MAX - 64) return MOE_ERR_UNSUPPORTED;
+    LinearArgs a = {};
+    a.T = T;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.f16 = d.dtype == MOE_F16;
+    a.res_f32 = res_f32;
+    a.act = d.act;
+    a.ldx = d.ldx;
+    a.ldw = d.ldw;
+    a.ldr = d.ldr;
+    a.ldy = d.ldy;
+    a.x = d_x;
+    a.w = d_w;
+    a.bias = d_bias;
+    a.res = d_residual;
+    a.y = d_y;
+    a.ctrl = static_cast<Ctrl*>(d_ws);
+    const cudaError_t err = launch_linear(a, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : err == cudaErrorInvalidConfiguration ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
 }
 
 moe_status moe_forward_timed(const moe_shape* shape, int32_t T, const void* d_packed, const uint16_t* d_x,

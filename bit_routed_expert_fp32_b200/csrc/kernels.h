@@ -204,6 +204,18 @@ cudaError_t launch_combine_pairs(int T, int k, int H, int n_rows, const float* r
 // gate-weighted unpermute-combine of the partial rows into y
 cudaError_t launch_combine(const FfnArgs& a, cudaStream_t s);
 
+// Dense matrix product with its epilogue (linear.cu); arguments as in moe_linear.
+struct LinearArgs {
+    int T, N, K;
+    bool f16, res_f32;
+    int act;
+    int64_t ldx, ldw, ldr, ldy;
+    const void *x, *w, *bias, *res;
+    void* y;
+    Ctrl* ctrl;
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+
 // Raises a kernel's dynamic shared memory limit on the current device.  The attribute
 // belongs to the device's context, so it is set before every launch rather than once
 // per process: a host-side call that enqueues nothing, cheap, and correct whichever

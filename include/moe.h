@@ -347,6 +347,48 @@ moe_status moe_forward_timed(const moe_shape* shape, int32_t T, const void* d_pa
                              moe_path path, void* d_ws, size_t ws_bytes, void* stream,
                              void* const* events, int32_t n_events);
 
+/* Dense matrix product with its epilogue: the products beside the packed experts whose
+ * weights are kept at 16 bits (a shared expert at full precision, the dense FFN layers of
+ * the same model, the projections around the layer).
+ *   a[t][n] = sum_k x[t][k] w[n][k] + bias[n]                    (fp32 sums)
+ *   y[t][n] = act(a[t][n]) + residual[t][n]                       (one rounding, to dtype)
+ * with, for MOE_ACT_SWIGLU, w of 2 out_features rows (and bias of as many values), the
+ * gate rows first, then the up rows:
+ *   y[t][n] = silu(a[t][n]) * a[t][out_features + n] + residual[t][n]
+ * silu(a) = a / (1 + e^-a); GELU is a (1 + erf(a / sqrt 2)) / 2; GELU_TANH its tanh form
+ * a (1 + tanh(sqrt(2 / pi) (a + 0.044715 a^3))) / 2. */
+typedef enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 } moe_dtype;
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_SILU = 2,
+    MOE_ACT_GELU = 3,
+    MOE_ACT_GELU_TANH = 4,
+    MOE_ACT_SWIGLU = 5
+} moe_act;
+typedef struct {
+    int32_t in_features;        /* K >= 1                                              */
+    int32_t out_features;       /* N >= 1 (columns of y)                               */
+    moe_dtype dtype;            /* of x, w, bias and y: MOE_BF16 or MOE_F16            */
+    moe_dtype residual_dtype;   /* of the residual: dtype or MOE_F32                   */
+    moe_act act;
+    int64_t ldx, ldw;           /* row strides in elements: >= K, multiples of 8       */
+    int64_t ldr, ldy;           /* row strides in elements: >= N                       */
+} moe_linear_desc;
+
+/* T tokens (rows of x and y).  d_x, d_w: 16-byte aligned; d_bias, d_residual: NULL for none;
+ * the rest aligned to its element.  d_ws is used for its control block only (4096 bytes are
+ * enough, cleared by moe_workspace_init): a wait that runs out is recorded there for
+ * moe_get_error.  The call keeps no state in it, so concurrent calls may share one.
+ * d_y may be d_residual (same type and stride: updated in place); y must not otherwise
+ * overlap an input (column slices of one buffer with one row stride may interleave).
+ * T = 0 is a no-op.  Values past 16-bit range become infinities, as the type rounds.
+ * MOE_ERR_INVALID_ARG: a null or unaligned pointer, a size, stride, type or activation
+ * outside the above, an overlap, ws_bytes < 4096.  MOE_ERR_UNSUPPORTED: a launch that the
+ * device cannot take (2 out_features or T past 2^31). */
+moe_status moe_linear(const moe_linear_desc* desc, int32_t T, const void* d_x, const void* d_w, const void* d_bias,
+                      const void* d_residual, void* d_y, void* d_ws, size_t ws_bytes, void* stream);
+
 /* The kernels that moe_route followed by moe_forward(shape, T, path) launch; host-only
  * (no device work, no CUDA call).  plan is a caller array of 4 int32:
  *   plan[0]  the kernels moe_forward runs: MOE_PATH_DECODE (separate gate/up, down and
