@@ -28,12 +28,13 @@ EXPORTS = ["moe_packed_size", "moe_pack_experts", "moe_requantize_q3_to_q2", "mo
            "moe_forward", "moe_forward_timed", "moe_get_error", "moe_decode_static", "moe_decode_static_get_error",
            "moe_workspace_set_test_stall", "moe_event_record", "moe_status_string", "moe_abi_version",
            "moe_route_fixed", "moe_gather_rows", "moe_combine_pairs", "moe_cache_size", "moe_cache_init",
-           "moe_cache_load", "moe_forward_plan", "moe_linear"]
+           "moe_cache_load", "moe_forward_plan", "moe_linear", "moe_route_scored"]
 # detail codes beside MOE_ERR_TIMEOUT / MOE_ERR_DEVICE_CHECK (high bits: what; low byte: where)
 DETAIL = {"WAIT_FULL": 0x100, "WAIT_EMPTY": 0x200, "DRAIN": 0x300, "HEADER": 0x400, "ROUTED_T": 0x500,
           "RANGE": 0x600, "TEST_STALL": 0x700, "LOOP_CAP": 0x800, "FORMAT": 0x900}
 FMT_TERNARY_DENSE = 3       # storage form of ternary experts (five codes per byte), see moe.h
 STATIC_WS_BYTES = 8 << 20
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1                                        # moe_score
 BF16, F16, F32 = 0, 1, 2                                                   # moe_dtype
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_SWIGLU = range(6)   # moe_act
 
@@ -55,6 +56,15 @@ class Routing(ctypes.Structure):
 
 class MatrixSrc(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("hi", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Router(ctypes.Structure):
+    """How moe_route_scored chooses experts from their scores (moe_router in moe.h)."""
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32),
+                ("group_top", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+    def __init__(self, score=SCORE_SOFTMAX, n_groups=1, top_groups=1, group_top=1, renormalise=True, scale=1.0):
+        super().__init__(score, n_groups, top_groups, group_top, int(renormalise), scale)
 
 
 class LinearDesc(ctypes.Structure):
@@ -95,6 +105,8 @@ def lib() -> ctypes.CDLL:
         L.moe_cache_size.argtypes = [sh, vp, i32, ctypes.POINTER(sz)]
         L.moe_cache_init.argtypes = [sh, vp, i32, vp, sz, vp]
         L.moe_cache_load.argtypes = [sh, vp, i32, vp, sz, vp, vp, i32, vp]
+        L.moe_route_scored.argtypes = [sh, ctypes.POINTER(Router), i32, vp, vp, vp, vp, ctypes.POINTER(Routing), vp,
+                                       sz, vp]
         L.moe_linear.argtypes = [ctypes.POINTER(LinearDesc), i32, vp, vp, vp, vp, vp, vp, sz, vp]
         L.moe_event_record.argtypes = [vp, vp]
         L.moe_status_string.argtypes = [ctypes.c_int]
@@ -296,6 +308,16 @@ def moe_route_fixed(cfg, T, x, ids, gates, rt: dict, ws, stream=None) -> None:
                                                      _stream(stream)))
 
 
+def moe_route_scored(cfg, router: Router, T, x, router_w, router_b, balance, rt: dict, ws, stream=None) -> None:
+    """moe_route with softmax or sigmoid scores, a balance bias (device float32 [E] or None)
+    that steers the choice only, expert groups and scaled weights."""
+    r = routing_struct(rt)
+    _check("moe_route_scored",
+           lib().moe_route_scored(ctypes.byref(_shape(cfg)), ctypes.byref(router), T, _ptr(x), _ptr(router_w),
+                                  _ptr(router_b), _ptr(balance), ctypes.byref(r), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)))
+
+
 def moe_gather_rows(src, index, divisor, dst, ws, n=None, stream=None) -> None:
     """dst[i] = src[index[i] // divisor] for the first n rows (bf16 [rows][H] tensors)."""
     n = index.numel() if n is None else n
@@ -387,10 +409,15 @@ def moe_status_string(st: int) -> str:
 
 
 class MoeLayer:
-    """Device-resident layer: packed experts, router, workspace and routing buffers."""
+    """Device-resident layer: packed experts, router, workspace and routing buffers.
+
+    router, balance: a scored router (moe_route_scored) in place of the softmax top-k.
+    shared: (w_gate_up [2 I_s][H], w_down [H][I_s]), bfloat16 device tensors of an expert kept
+    at 16 bits that every token uses (moe_linear): y = routed sum + w_down (silu(gate) * up),
+    the routed sum entering in fp32, so that y is rounded once."""
 
     def __init__(self, cfg, packed_host: np.ndarray, router_w: np.ndarray, router_b, max_tokens: int,
-                 device="cuda"):
+                 device="cuda", router: Router = None, balance=None, shared=None):
         import torch
         self.cfg = cfg
         self.device = device
@@ -398,18 +425,50 @@ class MoeLayer:
         self.router_w = torch.from_numpy(np.ascontiguousarray(router_w, np.float32)).to(device)
         self.router_b = None if router_b is None else torch.from_numpy(
             np.ascontiguousarray(router_b, np.float32)).to(device)
+        if balance is not None and router is None:
+            raise ValueError("MoeLayer: balance needs a router")
+        self.router = router
+        self.balance = None if balance is None else torch.from_numpy(
+            np.ascontiguousarray(balance, np.float32)).to(device)
         self.max_tokens = max_tokens
         self.ws = torch.empty(moe_workspace_size(cfg, max_tokens), dtype=torch.uint8, device=device)
         moe_workspace_init(self.ws)
         self.rt = alloc_routing(cfg, max_tokens, device)
+        self.shared = None
+        if shared is not None:
+            w_gu, w_dn = shared
+            if w_gu.shape[0] % 2 or w_gu.shape[1] != cfg.H or tuple(w_dn.shape) != (cfg.H, w_gu.shape[0] // 2):
+                raise ValueError(f"MoeLayer: shared must be [2 I][{cfg.H}] and [{cfg.H}][I], got {tuple(w_gu.shape)} "
+                                 f"and {tuple(w_dn.shape)}")
+            # rows of w_down and of h start on 16 bytes whatever the expert's width
+            n = w_dn.shape[1]
+            width = (n + 7) // 8 * 8
+            if w_dn.stride(0) % 8:
+                w_dn = torch.nn.functional.pad(w_dn, (0, width - n))[:, :n]
+            self.shared = (w_gu, w_dn)
+            self.shared_h = torch.empty((max_tokens, width), dtype=torch.bfloat16, device=device)
+            self.routed = torch.empty((max_tokens, cfg.H), dtype=torch.float32, device=device)
 
     def route(self, x, T=None, stream=None):
         T = x.shape[0] if T is None else T
-        moe_route(self.cfg, T, x, self.router_w, self.router_b, self.rt, self.ws, stream)
+        if self.router is not None:
+            moe_route_scored(self.cfg, self.router, T, x, self.router_w, self.router_b, self.balance, self.rt, self.ws,
+                             stream)
+        else:
+            moe_route(self.cfg, T, x, self.router_w, self.router_b, self.rt, self.ws, stream)
 
     def forward(self, x, y, T=None, path=PATH_AUTO, stream=None, events=None):
         T = x.shape[0] if T is None else T
-        moe_forward(self.cfg, T, self.packed, x, self.rt, y, path, self.ws, stream, events)
+        if self.shared is None:
+            moe_forward(self.cfg, T, self.packed, x, self.rt, y, path, self.ws, stream, events)
+            return
+        if path & OUT_F32:
+            raise ValueError("MoeLayer: a layer with a 16-bit shared expert writes bf16")
+        w_gu, w_dn = self.shared
+        moe_forward(self.cfg, T, self.packed, x, self.rt, self.routed, path | OUT_F32, self.ws, stream, events)
+        h = self.shared_h[:T, :w_dn.shape[1]]
+        moe_linear(x[:T], w_gu, h, self.ws, act=ACT_SWIGLU, stream=stream)
+        moe_linear(h, w_dn, y[:T], self.ws, residual=self.routed[:T], stream=stream)
 
     def __call__(self, x, path=PATH_AUTO, stream=None):
         import torch

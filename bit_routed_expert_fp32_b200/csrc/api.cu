@@ -2,6 +2,8 @@
 // layout and kernel launches.  Nothing here allocates memory or synchronises,
 // except moe_get_error, which is documented to.
 #include <cuda_runtime.h>
+#include <float.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -165,9 +167,37 @@ moe_status plan_forward(const moe_shape* shape, int64_t T, moe_path path, Forwar
     return MOE_OK;
 }
 
+// The router kernels' arguments (moe_route, moe_route_scored).
+static RouteArgs route_args(const moe_shape* shape, int32_t T, const uint16_t* d_x, const float* d_router_w,
+                     const float* d_router_b, const moe_routing* out, void* d_ws) {
+    const Ws w = ws_layout(shape, T);
+    uint8_t* ws = static_cast<uint8_t*>(d_ws);
+    RouteArgs a = {};     // every field not set below is zero (no fixed routing)
+    a.T = T;
+    a.H = shape->hidden;
+    a.E = shape->n_experts;
+    a.k = shape->top_k;
+    a.S = shape->n_shared;
+    a.x = d_x;
+    a.Wr = d_router_w;
+    a.bias = d_router_b;
+    a.logits = reinterpret_cast<float*>(ws + w.logits);
+    a.hist = reinterpret_cast<int32_t*>(ws + w.hist);
+    a.active = reinterpret_cast<int32_t*>(ws + w.active);
+    a.zx = reinterpret_cast<float*>(ws + w.zx);
+    // The decode operands are formed by the router only for the decode kernels that do
+    // not form them themselves (more than kFusedMaxT tokens).
+    a.ops = T <= kSmallT;                                 // the decode operands (the decode
+                                                          // path forms them itself above)
+    a.iq = T <= kFusedMaxT ? ws + w.iq : nullptr;         // and the integer records
+    a.ctrl = reinterpret_cast<Ctrl*>(ws + w.ctrl);
+    a.r = *out;
+    return a;
+}
+
 // Whether two strided matrices (base, rows, bytes of a row, row stride in bytes) share
 // memory.  Column slices of one buffer have one stride and interleave without sharing.
-bool overlap(const void* pa, int64_t ra, int64_t wa, int64_t la, const void* pb, int64_t rb, int64_t wb, int64_t lb) {
+static bool overlap(const void* pa, int64_t ra, int64_t wa, int64_t la, const void* pb, int64_t rb, int64_t wb, int64_t lb) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(pa), b = reinterpret_cast<uintptr_t>(pb);
     const uintptr_t ea = a + (uintptr_t)((ra - 1) * la + wa), eb = b + (uintptr_t)((rb - 1) * lb + wb);
     if (a >= eb || b >= ea) return false;
@@ -234,30 +264,30 @@ moe_status moe_route(const moe_shape* shape, int32_t T, const uint16_t* d_x, con
     const moe_status st = check_route_args(shape, T, d_x, d_router_w, out, d_ws, ws_bytes);
     if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
-    const Ws w = ws_layout(shape, T);
-    uint8_t* ws = static_cast<uint8_t*>(d_ws);
-    RouteArgs a = {};     // every field not set below is zero (no fixed routing)
-    a.T = T;
-    a.H = shape->hidden;
-    a.E = shape->n_experts;
-    a.k = shape->top_k;
-    a.S = shape->n_shared;
-    a.x = d_x;
-    a.Wr = d_router_w;
-    a.bias = d_router_b;
-    a.logits = reinterpret_cast<float*>(ws + w.logits);
-    a.hist = reinterpret_cast<int32_t*>(ws + w.hist);
-    a.active = reinterpret_cast<int32_t*>(ws + w.active);
-    a.zx = reinterpret_cast<float*>(ws + w.zx);
-    // The decode operands are formed by the router only for the decode kernels that do
-    // not form them themselves (more than kFusedMaxT tokens).
-    a.ops = T <= kSmallT;                                 // the decode operands (the decode
-                                                          // path forms them itself above)
-    a.iq = T <= kFusedMaxT ? ws + w.iq : nullptr;         // and the integer records
-    a.ctrl = reinterpret_cast<Ctrl*>(ws + w.ctrl);
-    a.r = *out;
+    const RouteArgs a = route_args(shape, T, d_x, d_router_w, d_router_b, out, d_ws);
     if (launch_route(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
+}
+
+moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, int32_t T, const uint16_t* d_x,
+                            const float* d_router_w, const float* d_router_b, const float* d_balance,
+                            const moe_routing* out, void* d_ws, size_t ws_bytes, void* stream) {
+    const moe_status st = check_route_args(shape, T, d_x, d_router_w, out, d_ws, ws_bytes);
+    if (st != MOE_OK) return st;
+    if (!router) return MOE_ERR_INVALID_ARG;
+    const int32_t E = shape->n_experts, G = router->n_groups;
+    if (((int)router->score != MOE_SCORE_SOFTMAX && (int)router->score != MOE_SCORE_SIGMOID) || G < 1 || G > 32 ||
+        E % G || router->top_groups < 1 || router->top_groups > G || router->group_top < 1 || router->group_top > 2 ||
+        router->group_top > E / G || router->top_groups * (E / G) < shape->top_k ||
+        (router->renormalise != 0 && router->renormalise != 1) || !(fabsf(router->scale) <= FLT_MAX))
+        return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_router_b) | reinterpret_cast<uintptr_t>(d_balance)) & 3)
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const RouteArgs a = route_args(shape, T, d_x, d_router_w, d_router_b, out, d_ws);
+    const ScoreArgs r = {router->score == MOE_SCORE_SIGMOID, G,
+                         router->top_groups, router->group_top, router->renormalise, router->scale, d_balance};
+    return launch_route_scored(a, r, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_route_fixed(const moe_shape* shape, int32_t T, const uint16_t* d_x, const int32_t* d_ids,

@@ -251,6 +251,36 @@ moe_status moe_route(const moe_shape* shape, int32_t T, const uint16_t* d_x,
                      const float* d_router_w, const float* d_router_b, const moe_routing* out,
                      void* d_ws, size_t ws_bytes, void* stream);
 
+/* Scored routing: moe_route with the choice of a balance-biased, grouped router.
+ *   L      as in moe_route (fp32: the exact sum, plus the logit bias, rounded)
+ *   s      = sigmoid(L[t,e]) or softmax_e(L[t,:]);  c = s + balance[e]
+ *   group  score = sum of the group_top largest c of its n_experts / n_groups consecutive
+ *          experts; the top_groups groups with the largest scores stay (equal -> lower group)
+ *   ids    = the k largest c among the experts of those groups, largest first (equal ->
+ *          lower id);  weights g[t,j] = s[ids[t,j]] (/ sum_j' s[ids[t,j']]) * scale
+ * The balance values steer the choice and leave the weights alone.  Scores and choice are
+ * formed in fp64 from the fp32 logits.  -infinity in balance switches an expert off: it is
+ * chosen (lowest id first) only where the kept groups have fewer than k others, and its
+ * group's score is -infinity where group_top reaches it; NaN counts as -infinity.  Where
+ * every chosen score is zero the renormalised weights are zero. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef struct {
+    moe_score score;
+    int32_t n_groups;       /* 1..32, a divisor of n_experts (1: no groups)                 */
+    int32_t top_groups;     /* 1..n_groups; top_groups * (n_experts / n_groups) >= top_k    */
+    int32_t group_top;      /* 1 or 2, at most the group's size                             */
+    int32_t renormalise;    /* 0 or 1                                                       */
+    float scale;            /* finite                                                       */
+} moe_router;
+
+/* Writes what moe_route writes (routing arrays, topk_w the weights above, and the schedule in
+ * d_ws that moe_forward reads).  d_balance: fp32 [E] on the device, or NULL.  Otherwise the
+ * arguments, rules and errors of moe_route; a router outside the above is
+ * MOE_ERR_INVALID_ARG. */
+moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, int32_t T, const uint16_t* d_x,
+                            const float* d_router_w, const float* d_router_b, const float* d_balance,
+                            const moe_routing* out, void* d_ws, size_t ws_bytes, void* stream);
+
 /* moe_route with the expert choice given instead of computed: for callers that route
  * elsewhere, such as the expert-parallel layer, whose GPUs each run only their own
  * experts on the token rows sent to them (every row with one expert, gate 1).  Writes
