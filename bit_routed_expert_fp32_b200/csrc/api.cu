@@ -389,6 +389,7 @@ moe_status moe_linear(const moe_linear_desc* desc, int32_t T, const void* d_x, c
     a.res = d_residual;
     a.y = d_y;
     a.ctrl = static_cast<Ctrl*>(d_ws);
+    a.num_ctas = sm_count();
     const cudaError_t err = launch_linear(a, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? MOE_OK : err == cudaErrorInvalidConfiguration ? MOE_ERR_UNSUPPORTED : MOE_ERR_CUDA;
 }

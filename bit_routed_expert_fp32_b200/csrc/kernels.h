@@ -224,6 +224,7 @@ struct LinearArgs {
     const void *x, *w, *bias, *res;
     void* y;
     Ctrl* ctrl;
+    int num_ctas;            // SMs of the current device
 };
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 

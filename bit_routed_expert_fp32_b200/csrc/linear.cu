@@ -34,7 +34,7 @@ struct LinKernelArgs {
     const void* bias;
     const void* res;
     void* y;
-    int vec;                 // 4 consecutive outputs of a row can be read and written at once
+    int vec, vec_res;        // 4 consecutive values of a row of y / the residual can be moved at once
     Ctrl* ctrl;
 };
 
@@ -59,6 +59,55 @@ __device__ inline float apply_act(int act, float a) {
         case MOE_ACT_GELU_TANH: return 0.5f * a * (1.f + tanhf(0.79788456f * (a + 0.044715f * a * a * a)));
     }
     return a;
+}
+
+// Up to four consecutive residual values (index i on; n valid) into r.
+template <bool F16>
+__device__ inline void load_res4(const void* res, int f32, bool vec, int64_t i, int n, float (&r)[4]) {
+    if (f32) {
+        const float* src = static_cast<const float*>(res) + i;
+        if (vec) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            r[0] = v.x;
+            r[1] = v.y;
+            r[2] = v.z;
+            r[3] = v.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) r[j] = src[j];
+        }
+    } else {
+        const uint16_t* src = static_cast<const uint16_t*>(res) + i;
+        if (vec) {
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            r[0] = to_f32<F16>(v.x & 0xFFFF);
+            r[1] = to_f32<F16>(v.x >> 16);
+            r[2] = to_f32<F16>(v.y & 0xFFFF);
+            r[3] = to_f32<F16>(v.y >> 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < n) r[j] = to_f32<F16>(src[j]);
+        }
+    }
+}
+// The output's one rounding, and up to four consecutive stores (n valid).
+template <bool F16>
+__device__ inline void store4(uint16_t* dst, bool vec, int n, const float (&o)[4]) {
+    const uint32_t a = from_f32<F16>(o[0]), b = from_f32<F16>(o[1]), c = from_f32<F16>(o[2]), d = from_f32<F16>(o[3]);
+    if (vec) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(a | (b << 16), c | (d << 16));
+    } else {
+        dst[0] = (uint16_t)a;
+        if (n > 1) dst[1] = (uint16_t)b;
+        if (n > 2) dst[2] = (uint16_t)c;
+        if (n > 3) dst[3] = (uint16_t)d;
+    }
+}
+// Whether groups of four values of a row (4-aligned columns) can be moved at once.
+inline bool vec4_ok(const void* base, int64_t ld, int size) {
+    return ld % 4 == 0 && reinterpret_cast<uintptr_t>(base) % (4 * size) == 0;
 }
 
 // Shared state of a CTA.
@@ -237,35 +286,23 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
                 a[pl][3] = v.w;
             }
             const int64_t t = t0 + tok;
-            uint16_t out[4];
+            float o[4], res[4] = {0.f, 0.f, 0.f, 0.f};
+            const bool full = n + 3 < p.N;
+            if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + n, p.N - n, res);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (n + j >= p.N) break;
                 float v = a[0][j];
-                if (p.bias) v += to_f32<F16>(static_cast<const uint16_t*>(p.bias)[n + j]);
+                if (p.bias && n + j < p.N) v += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + n + j));
                 if (GLU) {
                     float u = a[kPlanes - 1][j];
-                    if (p.bias) u += to_f32<F16>(static_cast<const uint16_t*>(p.bias)[p.N + n + j]);
+                    if (p.bias && n + j < p.N) u += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n + j));
                     v = silu_fast(v) * u;
                 } else {
                     v = apply_act(p.act, v);
                 }
-                if (p.res) {
-                    const int64_t ri = t * p.ldr + n + j;
-                    v += p.res_f32 ? static_cast<const float*>(p.res)[ri]
-                                   : to_f32<F16>(static_cast<const uint16_t*>(p.res)[ri]);
-                }
-                out[j] = from_f32<F16>(v);
+                o[j] = v + res[j];
             }
-            uint16_t* yp = static_cast<uint16_t*>(p.y) + t * p.ldy + n;
-            if (p.vec && n + 3 < p.N) {
-                *reinterpret_cast<uint2*>(yp) = make_uint2(out[0] | ((uint32_t)out[1] << 16),
-                                                           out[2] | ((uint32_t)out[3] << 16));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n + j < p.N) yp[j] = out[j];
-            }
+            store4<F16>(static_cast<uint16_t*>(p.y) + t * p.ldy + n, p.vec && full, p.N - n, o);
         }
     }
     // no CTA's shared memory goes away while another reads it
@@ -288,7 +325,8 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
     p.res = a.res;
     p.y = a.y;
     p.ctrl = a.ctrl;
-    p.vec = a.ldy % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
+    p.vec = vec4_ok(a.y, a.ldy, 2);
+    p.vec_res = vec4_ok(a.res, a.ldr, a.res_f32 ? 4 : 2);
     const int ttiles = (a.T + max_nt - 1) / max_nt;
     p.nt = ((a.T + ttiles - 1) / ttiles + 15) & ~15;
     p.tmem_cols = 32;
@@ -332,9 +370,323 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, linear_kernel<F16, GLU>, p, wm, xm);
 }
 
+// ---------------------------------------------------------------- many tokens
+// Tiles of 256 tokens x 256 weight rows by pairs of CTAs (cta_group::2: D[token][feature],
+// each CTA 128 tokens, half of the weight rows from each CTA's shared memory), persistent
+// over the tiles, two accumulators in tensor memory, so that the epilogue of a tile overlaps
+// the main loop of the next.  With SwiGLU the 256 weight rows are the gate and the up rows
+// of 128 features (one CTA brings the former, the other the latter): both values of an
+// output lie 128 columns apart in one thread's lane.
+// Epilogue (4 warps, one per 32 token rows): 32 columns at a time through a padded
+// shared-memory square, so that residual loads and stores run along the rows.
+constexpr int kPairThreads = 256, kPairTok = 256, kPairStages = 6, kPairCols = 512;
+constexpr int kPairStageBytes = 2 * 128 * kBK * 2;      // a CTA's share: 128 token rows, 128 weight rows
+constexpr int kSqLd = 36;                               // floats per row of the epilogue's square
+constexpr size_t kPairSmem = 227 * 1024 - 1024;         // the whole SM (with the static part): 512 columns
+
+struct PairArgs {
+    int T, N, K, act, res_f32;
+    int ttiles, ftiles;      // tiles along tokens and outputs
+    int group;               // token tiles that share a sweep over the outputs (L2 reuse)
+    int64_t ldr, ldy;
+    const void* bias;
+    const void* res;
+    void* y;
+    int vec;                 // 4 consecutive values of a row of y can be written at once
+    int vec_res;             // 4 consecutive residual values can be read at once
+    Ctrl* ctrl;
+};
+
+struct PairShared {
+    uint64_t full[kPairStages], empty_[kPairStages], acc_full[2], acc_empty[2], drained, stall_bar;
+    uint32_t tmem;
+    int abort_flag;
+};
+
+// Bounded wait that gives up at once when either CTA of the pair has given up.
+__device__ inline bool pair_wait(PairShared& S, uint64_t* bar, uint32_t parity, Ctrl* ctrl, uint32_t detail) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!ld_volatile(S.abort_flag)) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > kWaitLimit) {
+            st_volatile(S.abort_flag, 1);
+            st_peer_u32(map_peer(smem_u32(&S.abort_flag), cluster_rank() ^ 1), 1);
+            report_error(ctrl, MOE_ERR_TIMEOUT, detail);
+        }
+    }
+    return false;
+}
+
+__device__ inline void pair_tile(const PairArgs& p, int tile, int& tt, int& ft) {
+    const int per = p.group * p.ftiles, g = tile / per, r = tile - g * per;
+    const int rows = min(p.group, p.ttiles - g * p.group);
+    ft = r / rows;
+    tt = g * p.group + r - ft * rows;
+}
+
+template <bool F16, bool GLU>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ PairArgs p, const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap xmap) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ PairShared S;
+    constexpr int kOut = GLU ? 128 : 256;                // outputs per tile
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int n_tiles = p.ttiles * p.ftiles, chunks = (p.K + kBK - 1) / kBK;
+    const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        prefetch_map(&wmap);
+        prefetch_map(&xmap);
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty_[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.acc_full[i], 1);
+            mbar_init(&S.acc_empty[i], 8);               // the epilogue warps of both CTAs
+        }
+        mbar_init(&S.drained, 1);
+        mbar_init(&S.stall_bar, 1);                     // nothing ever arrives on it
+        fence_mbar_init();
+        S.abort_flag = 0;
+    }
+    griddep_wait();
+    if (warp == 2) tmem_alloc_pair(&S.tmem, kPairCols);
+    fence_before();
+    __syncthreads();
+    cluster_sync();
+    fence_after();
+    griddep_launch_dependents();
+    const uint32_t tmem = S.tmem;
+
+    if (warp == 0) {
+        // ---- producer: this CTA's rows, counted on the leader's barrier -----------------
+        int slot = 0, issued = 0;
+        uint32_t par = 1;
+        bool stop = false;
+        for (int tile = pair; tile < n_tiles && !stop; tile += n_pairs) {
+            int tt, ft;
+            pair_tile(p, tile, tt, ft);
+            const int trow = tt * kPairTok + rank * 128;
+            const int wrow = GLU ? rank * p.N + ft * kOut : ft * kOut + rank * 128;
+            for (int kc = 0; kc < chunks; ++kc) {
+                if (!__all_sync(0xffffffffu, pair_wait(S, &S.empty_[slot], par, p.ctrl, kDetWaitEmpty | 0x62))) {
+                    stop = true;
+                    break;
+                }
+                if (elect_one()) {
+                    uint8_t* dst = smem + (size_t)slot * kPairStageBytes;
+                    const uint32_t bar = map_peer(smem_u32(&S.full[slot]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&S.full[slot], 2 * kPairStageBytes);
+                    tma_load_2d_pair(dst, &xmap, kc * kBK, trow, bar);
+                    tma_load_2d_pair(dst + 128 * kBK * 2, &wmap, kc * kBK, wrow, bar);
+                }
+                __syncwarp();
+                ++issued;
+                if (++slot == kPairStages) {
+                    slot = 0;
+                    par ^= 1;
+                }
+            }
+        }
+        // after an abort no copy may still target either CTA's shared memory at exit: the
+        // leader, on whose barriers the bytes of both count, waits (bounded) for the last
+        // phase issued on every slot; the other CTA, which may have issued past the leader,
+        // gives its last copies (microseconds) some half a millisecond
+        if (stop && lane == 0) {
+            if (rank == 0) {
+                for (int d = 0; d < kPairStages && d < issued; ++d) {
+                    const int i = issued - 1 - d;
+                    if (!mbar_wait_bounded(&S.full[i % kPairStages], (uint32_t)(i / kPairStages) & 1, kWaitLimit)) {
+                        report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetDrain | 0x62);
+                        break;
+                    }
+                }
+            } else {
+                const long long c0 = clock64();
+                while (clock64() - c0 < 1000000) __nanosleep(1000);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMA issuer (the leader's) ----------------------------------------------------
+        constexpr uint32_t idesc = instr_desc(F16, 256, 256);
+        const uint64_t ad0 = smem_desc(smem_u32(smem)), bd0 = smem_desc(smem_u32(smem) + 128 * kBK * 2);
+        const uint32_t stall = p.ctrl->test_stall;
+        bool ok = true;
+        if (stall) {
+            // failure-path tests: a bounded wait on a barrier that nothing completes
+            bool got = false;
+            if (lane == 0) got = mbar_wait_bounded(&S.stall_bar, 0, stall);
+            if (!__shfl_sync(0xffffffffu, got, 0)) {
+                if (lane == 0) {
+                    report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetTestStall | 0x62);
+                    st_volatile(S.abort_flag, 1);
+                    st_peer_u32(map_peer(smem_u32(&S.abort_flag), 1), 1);
+                }
+                ok = false;
+            }
+            __syncwarp();
+        }
+        int slot = 0, n = 0;
+        uint32_t par = 0;
+        for (int tile = pair; tile < n_tiles && ok; tile += n_pairs, ++n) {
+            const int buf = n & 1;
+            ok = pair_wait(S, &S.acc_empty[buf], (uint32_t)((n >> 1) & 1) ^ 1, p.ctrl, kDetWaitEmpty | 0x63);
+            ok = __all_sync(0xffffffffu, ok);
+            fence_after();
+            for (int kc = 0; kc < chunks && ok; ++kc) {
+                ok = pair_wait(S, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x62);
+                ok = __all_sync(0xffffffffu, ok);
+                fence_after();
+                if (ok && elect_one()) {
+                    const uint64_t off = (uint64_t)slot * (kPairStageBytes >> 4);
+#pragma unroll
+                    for (int k16 = 0; k16 < kBK / 16; ++k16)
+                        umma_ss_pair(tmem + buf * 256, ad0 + off + 2 * k16, bd0 + off + 2 * k16, idesc,
+                                     (kc | k16) != 0 ? 1u : 0u);
+                    umma_commit_pair(&S.empty_[slot]);
+                }
+                __syncwarp();
+                if (++slot == kPairStages) {
+                    slot = 0;
+                    par ^= 1;
+                }
+            }
+            if (ok && elect_one()) umma_commit_pair(&S.acc_full[buf]);
+            __syncwarp();
+        }
+        if (elect_one()) umma_commit_pair(&S.drained);
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---- epilogue -----------------------------------------------------------------
+        const int q = warp & 3;                           // tensor-memory lanes 32q .. 32q+31
+        float* const sq = reinterpret_cast<float*>(smem + (size_t)kPairStages * kPairStageBytes) + q * 32 * kSqLd;
+        const int lr = lane >> 3, lc = 4 * (lane & 7);     // row and column of the square, along the rows
+        int n = 0;
+        for (int tile = pair; tile < n_tiles; tile += n_pairs, ++n) {
+            int tt, ft;
+            pair_tile(p, tile, tt, ft);
+            const int buf = n & 1;
+            if (!__all_sync(0xffffffffu,
+                            pair_wait(S, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
+                break;
+            fence_after();
+            const uint32_t tl = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
+            const int t0 = tt * kPairTok + rank * 128 + 32 * q;
+            const int rows = min(32, p.T - t0);           // may be <= 0
+            for (int c0 = 0; c0 < kOut; c0 += 32) {
+                const int n0 = ft * kOut + c0;
+                if (n0 >= p.N) break;
+                uint32_t v[32];
+                tmem_ld32(tl + c0, v);
+                if (GLU) {
+                    uint32_t u[32];
+                    tmem_ld32(tl + 128 + c0, u);
+                    ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        float a = __uint_as_float(v[j]), b = __uint_as_float(u[j]);
+                        if (p.bias && n0 + j < p.N) {
+                            a += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + n0 + j));
+                            b += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n0 + j));
+                        }
+                        v[j] = __float_as_uint(silu_fast(a) * b);
+                    }
+                } else {
+                    ld_wait();
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(sq + lane * kSqLd + 4 * j) =
+                        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                __syncwarp();
+                const int nc = n0 + lc;
+                if (nc < p.N) {
+                    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+                    if (!GLU && p.bias) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (nc + j < p.N) bias[j] = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + nc + j));
+                    }
+                    const bool full = nc + 3 < p.N;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + lr;
+                        if (r >= rows) break;
+                        const int64_t t = t0 + r;
+                        const float4 f = *reinterpret_cast<const float4*>(sq + r * kSqLd + lc);
+                        float o[4] = {f.x, f.y, f.z, f.w};
+                        float res[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + nc, p.N - nc, res);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[j] = (GLU ? o[j] : apply_act(p.act, o[j] + bias[j])) + res[j];
+                        store4<F16>(static_cast<uint16_t*>(p.y) + t * p.ldy + nc, p.vec && full, p.N - nc, o);
+                    }
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(map_peer(smem_u32(&S.acc_empty[buf]), 0));
+        }
+    }
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    // every MMA issued has completed (the commit arrives in both CTAs)
+    if (warp == 1 && !mbar_wait_bounded(&S.drained, 0, kWaitLimit))
+        report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetDrain | 0x63);
+    __syncwarp();
+    cluster_sync();                     // both CTAs are done with each other's memory
+    fence_after();
+    if (warp == 2) tmem_dealloc_pair(tmem, kPairCols);
+}
+
+template <bool F16, bool GLU>
+cudaError_t launch_pair(const LinearArgs& a, cudaStream_t s) {
+    constexpr int kOut = GLU ? 128 : 256;
+    PairArgs p = {};
+    p.T = a.T;
+    p.N = a.N;
+    p.K = a.K;
+    p.act = a.act;
+    p.res_f32 = a.res_f32;
+    p.ldr = a.ldr;
+    p.ldy = a.ldy;
+    p.bias = a.bias;
+    p.res = a.res;
+    p.y = a.y;
+    p.ctrl = a.ctrl;
+    p.vec = vec4_ok(a.y, a.ldy, 2);
+    p.vec_res = vec4_ok(a.res, a.ldr, a.res_f32 ? 4 : 2);
+    p.ttiles = (a.T + kPairTok - 1) / kPairTok;
+    p.ftiles = (a.N + kOut - 1) / kOut;
+    p.group = 8;
+    if ((int64_t)p.ttiles * p.ftiles > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+    CUtensorMap wm, xm;
+    if (!make_map(&wm, F16, a.w, (int64_t)(GLU ? 2 : 1) * a.N, a.K, a.ldw, 128) ||
+        !make_map(&xm, F16, a.x, a.T, a.K, a.ldx, 128))
+        return cudaErrorInvalidConfiguration;
+    cudaError_t err = set_smem_limit(linear_pair_kernel<F16, GLU>, kPairSmem);
+    if (err != cudaSuccess) return err;
+    const int pairs = p.ttiles * p.ftiles < a.num_ctas / 2 ? p.ttiles * p.ftiles : a.num_ctas / 2;
+    return launch_pdl(linear_pair_kernel<F16, GLU>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, p, wm, xm);
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+    if (a.T >= 512) {
+        if (a.act == MOE_ACT_SWIGLU) return a.f16 ? launch_pair<true, true>(a, s) : launch_pair<false, true>(a, s);
+        return a.f16 ? launch_pair<true, false>(a, s) : launch_pair<false, false>(a, s);
+    }
     if (a.act == MOE_ACT_SWIGLU) return a.f16 ? launch<true, true>(a, s) : launch<false, true>(a, s);
     return a.f16 ? launch<true, false>(a, s) : launch<false, false>(a, s);
 }

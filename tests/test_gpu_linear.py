@@ -133,7 +133,7 @@ def test_output_widths(T, N, act):
 
 @pytest.mark.parametrize("T,K,N,act", [(1, 7168, 2048, 5), (1, 2048, 7168, 0), (16, 7168, 4096, 2), (64, 4096, 1024, 3),
                                        (130, 1992, 4999, 4), (1000, 2048, 2048, 5), (2049, 1024, 1100, 0),
-                                       (4096, 512, 2304, 5), (3001, 712, 4100, 1)])
+                                       (4096, 512, 2304, 5), (3001, 712, 4100, 1), (8000, 320, 5000, 0), (5121, 136, 2600, 5)])
 def test_larger(T, K, N, act):
     run(T, K, N, act, "bf16", seed=T + N, residual="same", pad=16)
 
@@ -224,7 +224,7 @@ def test_empty_batch_is_a_no_op():
     moe.moe_linear(x, w, torch.empty((0, 8), dtype=torch.bfloat16, device="cuda"), _ws())
 
 
-@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("T", [1, 300, 2000])
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T):
     import torch
     moe = _moe()
