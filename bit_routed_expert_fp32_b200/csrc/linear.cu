@@ -110,6 +110,23 @@ inline bool vec4_ok(const void* base, int64_t ld, int size) {
     return ld % 4 == 0 && reinterpret_cast<uintptr_t>(base) % (4 * size) == 0;
 }
 
+// The activation of a thread's 8 x 4 values, the choice outside the loops.
+__device__ inline void apply_act_all(int act, float (&o)[8][4]) {
+#define MOE_ACT_LOOP(A)                                                                      \
+    case A:                                                                                  \
+        _Pragma("unroll") for (int i = 0; i < 8; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j) \
+            o[i][j] = apply_act(A, o[i][j]);                                                 \
+        break;
+    switch (act) {
+        MOE_ACT_LOOP(MOE_ACT_RELU)
+        MOE_ACT_LOOP(MOE_ACT_SILU)
+        MOE_ACT_LOOP(MOE_ACT_GELU)
+        MOE_ACT_LOOP(MOE_ACT_GELU_TANH)
+        default: break;
+    }
+#undef MOE_ACT_LOOP
+}
+
 // Shared state of a CTA.
 struct LinShared {
     uint64_t full[kMaxStages], empty_[kMaxStages], done, stall_bar;
@@ -377,11 +394,13 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
 // the main loop of the next.  With SwiGLU the 256 weight rows are the gate and the up rows
 // of 128 features (one CTA brings the former, the other the latter): both values of an
 // output lie 128 columns apart in one thread's lane.
-// Epilogue (4 warps, one per 32 token rows): 32 columns at a time through a padded
-// shared-memory square, so that residual loads and stores run along the rows.
-constexpr int kPairThreads = 256, kPairTok = 256, kPairStages = 6, kPairCols = 512;
+// Epilogue (8 warps, two per 32 token rows, each half of the columns): 32 columns at a time
+// through a shared-memory square (16-byte pieces swizzled by the row, so that both directions
+// are free of bank conflicts), after which loads and stores run along the rows; the residual
+// of the next 32 columns is on its way meanwhile.
+constexpr int kPairThreads = 384, kPairTok = 256, kPairStages = 6, kPairCols = 512;
+constexpr int kPairEpi = 8;                             // epilogue warps (warps 4 .. 11)
 constexpr int kPairStageBytes = 2 * 128 * kBK * 2;      // a CTA's share: 128 token rows, 128 weight rows
-constexpr int kSqLd = 36;                               // floats per row of the epilogue's square
 constexpr size_t kPairSmem = 227 * 1024 - 1024;         // the whole SM (with the static part): 512 columns
 
 struct PairArgs {
@@ -449,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.acc_full[i], 1);
-            mbar_init(&S.acc_empty[i], 8);               // the epilogue warps of both CTAs
+            mbar_init(&S.acc_empty[i], 2 * kPairEpi);    // the epilogue warps of both CTAs
         }
         mbar_init(&S.drained, 1);
         mbar_init(&S.stall_bar, 1);                     // nothing ever arrives on it
@@ -566,69 +585,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ---- epilogue -----------------------------------------------------------------
-        const int q = warp & 3;                           // tensor-memory lanes 32q .. 32q+31
-        float* const sq = reinterpret_cast<float*>(smem + (size_t)kPairStages * kPairStageBytes) + q * 32 * kSqLd;
-        const int lr = lane >> 3, lc = 4 * (lane & 7);     // row and column of the square, along the rows
+        const int q = warp & 3, half = (warp - 4) >> 2;   // tensor-memory lanes 32q .. 32q+31; columns
+        constexpr int kCols = kOut / 2;                   // of this warp
+        float4* const sq = reinterpret_cast<float4*>(smem + (size_t)kPairStages * kPairStageBytes) + (warp - 4) * 256;
+        const int lr = lane >> 3, c4 = lane & 7;          // row (of 4) and 16-byte piece, along the rows
+        const bool res16 = p.res && !p.res_f32;
         int n = 0;
         for (int tile = pair; tile < n_tiles; tile += n_pairs, ++n) {
             int tt, ft;
             pair_tile(p, tile, tt, ft);
             const int buf = n & 1;
+            const int t0 = tt * kPairTok + rank * 128 + 32 * q, nb = ft * kOut + half * kCols;
+            // whole tiles with aligned rows move four values at a time without checks
+            const bool whole = t0 + 32 <= p.T && nb + kCols <= p.N && p.vec && (!p.res || p.vec_res);
+            uint4 rbuf[8];
+            auto load_res = [&](int c0) {
+                const int64_t at = (int64_t)(t0 + lr) * p.ldr + nb + c0 + 4 * c4;
+                if (res16) {
+                    const uint16_t* src = static_cast<const uint16_t*>(p.res) + at;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * i * p.ldr);
+                        rbuf[i].x = v.x;
+                        rbuf[i].y = v.y;
+                    }
+                } else {
+                    const float* src = static_cast<const float*>(p.res) + at;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) rbuf[i] = *reinterpret_cast<const uint4*>(src + 4 * i * p.ldr);
+                }
+            };
+            if (whole && p.res) load_res(0);
             if (!__all_sync(0xffffffffu,
                             pair_wait(S, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
                 break;
             fence_after();
-            const uint32_t tl = tmem + buf * 256 + ((uint32_t)(32 * q) << 16);
-            const int t0 = tt * kPairTok + rank * 128 + 32 * q;
-            const int rows = min(32, p.T - t0);           // may be <= 0
-            for (int c0 = 0; c0 < kOut; c0 += 32) {
-                const int n0 = ft * kOut + c0;
+            const uint32_t tl = tmem + buf * 256 + half * kCols + ((uint32_t)(32 * q) << 16);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kCols; c0 += 32) {
+                const int n0 = nb + c0, nc = n0 + 4 * c4;
                 if (n0 >= p.N) break;
                 uint32_t v[32];
                 tmem_ld32(tl + c0, v);
+                ld_wait();
                 if (GLU) {
+                    // both accumulators' values of an output are in one lane
                     uint32_t u[32];
                     tmem_ld32(tl + 128 + c0, u);
                     ld_wait();
+                    if (p.bias) {
+                        const uint16_t* bp = static_cast<const uint16_t*>(p.bias) + n0;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        float a = __uint_as_float(v[j]), b = __uint_as_float(u[j]);
-                        if (p.bias && n0 + j < p.N) {
-                            a += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + n0 + j));
-                            b += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n0 + j));
-                        }
-                        v[j] = __float_as_uint(silu_fast(a) * b);
+                        for (int j = 0; j < 32; ++j)
+                            if (n0 + j < p.N) {
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) + to_f32<F16>(__ldg(bp + j)));
+                                u[j] = __float_as_uint(__uint_as_float(u[j]) + to_f32<F16>(__ldg(bp + p.N + j)));
+                            }
                     }
-                } else {
-                    ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __float_as_uint(silu_fast(__uint_as_float(v[j])) * __uint_as_float(u[j]));
                 }
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(sq + lane * kSqLd + 4 * j) =
-                        make_uint4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    sq[lane * 8 + (j ^ (lane & 7))] =
+                        make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                    __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
                 __syncwarp();
-                const int nc = n0 + lc;
-                if (nc < p.N) {
-                    float bias[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (!GLU && p.bias) {
+                float o[8][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (nc + j < p.N) bias[j] = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + nc + j));
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + lr;
+                    const float4 f = sq[r * 8 + (c4 ^ (r & 7))];
+                    o[i][0] = f.x;
+                    o[i][1] = f.y;
+                    o[i][2] = f.z;
+                    o[i][3] = f.w;
+                }
+                if (!GLU) {
+                    if (p.bias) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float b =
+                                nc + j < p.N ? to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + nc + j)) : 0.f;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i][j] += b;
+                        }
                     }
+                    apply_act_all(p.act, o);
+                }
+                uint16_t* yp = static_cast<uint16_t*>(p.y) + (int64_t)(t0 + lr) * p.ldy + nc;
+                if (whole) {
+                    if (p.res) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (res16) {
+                                o[i][0] += to_f32<F16>(rbuf[i].x & 0xFFFF);
+                                o[i][1] += to_f32<F16>(rbuf[i].x >> 16);
+                                o[i][2] += to_f32<F16>(rbuf[i].y & 0xFFFF);
+                                o[i][3] += to_f32<F16>(rbuf[i].y >> 16);
+                            } else {
+                                o[i][0] += __uint_as_float(rbuf[i].x);
+                                o[i][1] += __uint_as_float(rbuf[i].y);
+                                o[i][2] += __uint_as_float(rbuf[i].z);
+                                o[i][3] += __uint_as_float(rbuf[i].w);
+                            }
+                        }
+                        if (c0 + 32 < kCols) load_res(c0 + 32);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) store4<F16>(yp + 4 * i * p.ldy, true, 4, o[i]);
+                } else if (nc < p.N) {
                     const bool full = nc + 3 < p.N;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + lr;
-                        if (r >= rows) break;
-                        const int64_t t = t0 + r;
-                        const float4 f = *reinterpret_cast<const float4*>(sq + r * kSqLd + lc);
-                        float o[4] = {f.x, f.y, f.z, f.w};
+                        const int64_t t = t0 + 4 * i + lr;
+                        if (t >= p.T) break;
                         float res[4] = {0.f, 0.f, 0.f, 0.f};
                         if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + nc, p.N - nc, res);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) o[j] = (GLU ? o[j] : apply_act(p.act, o[j] + bias[j])) + res[j];
-                        store4<F16>(static_cast<uint16_t*>(p.y) + t * p.ldy + nc, p.vec && full, p.N - nc, o);
+                        for (int j = 0; j < 4; ++j) o[i][j] += res[j];
+                        store4<F16>(yp + 4 * i * p.ldy, p.vec && full, p.N - nc, o[i]);
                     }
                 }
             }
