@@ -4,12 +4,13 @@
 //
 // One tile is 128 output features x NT tokens, D[feature][token] = W_tile x^T on tcgen05
 // with the weights as the A operand: a tile has its full M whatever the token count, so one
-// token costs the same weight bytes as any other count up to NT.  With SwiGLU the tile has
-// two accumulators, the gate rows' and the up rows' of the same features, so that a thread
-// holds both values of an output.  K is cut over the CTAs of a cluster when the tiles alone
-// do not fill the GPU; each CTA leaves its fp32 sums in its shared memory and every CTA of
-// the cluster adds a share of the tile from all of them, in part order (no atomics: the
-// result does not depend on timing), and applies the epilogue.
+// token costs the same weight bytes as any other count up to NT.  With SwiGLU the tile's 128
+// weight rows are the gate and the up rows of 64 features.  K is cut over the CTAs of a
+// cluster when the tiles alone do not fill the GPU; each CTA leaves its fp32 sums in its
+// shared memory and every CTA of the cluster adds a share of the tile from all of them, in
+// part order (no atomics: the result does not depend on timing), and applies the epilogue.
+// Sending the sums to the CTA that adds them, instead of its reading them, measured slower
+// (one token, 2048 -> 7168: 10.4 against 9.0 us): the barrier then waits for remote stores.
 #include "tc5.cuh"
 
 namespace moe {
@@ -18,9 +19,10 @@ namespace {
 using namespace tc5;
 
 constexpr int kFeat = 128;                 // output features per tile
-constexpr int kLinThreads = 128;
+constexpr int kLinThreads = 256;
 constexpr int kTileBytes = kFeat * kBK * 2;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 4;
+constexpr int kMaxSplit = 8;               // K parts: the CTAs of a cluster (the portable size)
 
 struct LinKernelArgs {
     int T, N, K;
@@ -146,22 +148,22 @@ __device__ inline bool wait_or_flag(LinShared& S, uint64_t* bar, uint32_t parity
 }
 
 template <bool F16, bool GLU>
-__global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_constant__ LinKernelArgs p,
+__global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_constant__ LinKernelArgs p,
                                                              const __grid_constant__ CUtensorMap wmap,
                                                              const __grid_constant__ CUtensorMap xmap) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ LinShared S;
-    constexpr int kPlanes = GLU ? 2 : 1;
+    constexpr int kOut = GLU ? kFeat / 2 : kFeat;       // outputs per tile
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = p.split > 1 ? (int)cluster_rank() : 0;
     const int tile = blockIdx.x / p.split, tt = tile / p.ftiles;
-    const int f0 = (tile - tt * p.ftiles) * kFeat, t0 = tt * p.nt;
+    const int f0 = (tile - tt * p.ftiles) * kOut, t0 = tt * p.nt;
     const int ntok = min(p.nt, p.T - t0);
     const int chunks = (p.K + kBK - 1) / kBK;
     const int kc0 = (int)((int64_t)part * chunks / p.split), kc1 = (int)((int64_t)(part + 1) * chunks / p.split);
     const int n_stage = kc1 - kc0;
-    const int stage_bytes = kPlanes * kTileBytes + p.nt * kBK * 2;
+    const int stage_bytes = kTileBytes + p.nt * kBK * 2;
 
     if (threadIdx.x == 0) {
         prefetch_map(&wmap);
@@ -195,8 +197,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
                 uint8_t* dst = smem + (size_t)s * stage_bytes;
                 mbar_arrive_expect_tx(&S.full[s], stage_bytes);
                 tma_load_2d(dst, &wmap, (kc0 + i) * kBK, f0, &S.full[s]);
-                if (GLU) tma_load_2d(dst + kTileBytes, &wmap, (kc0 + i) * kBK, p.N + f0, &S.full[s]);
-                tma_load_2d(dst + kPlanes * kTileBytes, &xmap, (kc0 + i) * kBK, t0, &S.full[s]);
+                if (GLU) tma_load_2d(dst + kTileBytes / 2, &wmap, (kc0 + i) * kBK, p.N + f0, &S.full[s]);
+                tma_load_2d(dst + kTileBytes, &xmap, (kc0 + i) * kBK, t0, &S.full[s]);
             }
             __syncwarp();
             issued = i + 1;
@@ -236,13 +238,10 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
             fence_after();
             if (ok && elect_one()) {
                 const uint32_t base = smem_u32(smem + (size_t)s * stage_bytes);
-                const uint64_t ad = smem_desc(base), bd = smem_desc(base + kPlanes * kTileBytes);
+                const uint64_t ad = smem_desc(base), bd = smem_desc(base + kTileBytes);
 #pragma unroll
-                for (int k16 = 0; k16 < kBK / 16; ++k16) {
-                    const uint32_t acc = (i | k16) != 0 ? 1u : 0u;
-                    umma_ss(tmem, ad + 2 * k16, bd + 2 * k16, idesc, acc);
-                    if (GLU) umma_ss(tmem + p.nt, ad + (kTileBytes >> 4) + 2 * k16, bd + 2 * k16, idesc, acc);
-                }
+                for (int k16 = 0; k16 < kBK / 16; ++k16)
+                    umma_ss(tmem, ad + 2 * k16, bd + 2 * k16, idesc, (i | k16) != 0 ? 1u : 0u);
                 umma_commit(&S.empty_[s]);
             }
             __syncwarp();
@@ -256,21 +255,19 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
     }
     __syncthreads();                                    // and the producer's copies are in
     fence_after();
-    // this CTA's sums, [plane][token][feature] fp32 over the stages' memory
+    // this CTA's sums, [token][weight row of the tile] fp32 over the stages' memory
     float* sums = reinterpret_cast<float*>(smem);
     const bool ok = !ld_volatile(S.abort_flag);
     if (ok) {
-        const uint32_t tl = tmem + ((uint32_t)(32 * warp) << 16);
+        // warps w and w + 4 share the lanes 32 (w % 4) .., taking 16 columns in turn
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        for (int c = 16 * (warp >> 2); c < ntok; c += 32) {
+            uint32_t v[16];
+            tmem_ld16(tl + c, v);
+            ld_wait();
 #pragma unroll
-        for (int pl = 0; pl < kPlanes; ++pl)
-            for (int c = 0; c < ntok; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(tl + pl * p.nt + c, v);
-                ld_wait();
-#pragma unroll
-                for (int u = 0; u < 16; ++u)
-                    sums[(size_t)(pl * p.nt + c + u) * kFeat + threadIdx.x] = __uint_as_float(v[u]);
-            }
+            for (int u = 0; u < 16; ++u) sums[(size_t)(c + u) * kFeat + (threadIdx.x & 127)] = __uint_as_float(v[u]);
+        }
     }
     fence_before();
     __syncthreads();
@@ -279,41 +276,44 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
     if (ok) {
         const uint32_t sbase = smem_u32(sums);
-        for (int i = part * kLinThreads + threadIdx.x; i < ntok * (kFeat / 4); i += p.split * kLinThreads) {
-            const int tok = i / (kFeat / 4), f = 4 * (i % (kFeat / 4)), n = f0 + f;
-            if (n >= p.N) continue;
-            float a[kPlanes][4];
+        // four sums from every part, in part order
+        auto total = [&](int row, float(&a)[4]) {
+            const uint32_t at = sbase + (uint32_t)row * 4;
+            float4 v[kMaxSplit];
 #pragma unroll
-            for (int pl = 0; pl < kPlanes; ++pl) {
-                const uint32_t at = sbase + (uint32_t)(((pl * p.nt + tok) * kFeat + f) * 4);
-                float4 v = *reinterpret_cast<const float4*>(sums + (size_t)(pl * p.nt + tok) * kFeat + f);
-                if (p.split > 1) {
-                    v = ld_peer_v4(map_peer(at, 0));
-                    for (int q = 1; q < p.split; ++q) {
-                        const float4 w = ld_peer_v4(map_peer(at, q));
-                        v.x += w.x;
-                        v.y += w.y;
-                        v.z += w.z;
-                        v.w += w.w;
-                    }
+            for (int q = 0; q < kMaxSplit; ++q)
+                if (q < p.split) v[q] = ld_peer_v4(map_peer(at, q));
+            a[0] = v[0].x;
+            a[1] = v[0].y;
+            a[2] = v[0].z;
+            a[3] = v[0].w;
+#pragma unroll
+            for (int q = 1; q < kMaxSplit; ++q)
+                if (q < p.split) {
+                    a[0] += v[q].x;
+                    a[1] += v[q].y;
+                    a[2] += v[q].z;
+                    a[3] += v[q].w;
                 }
-                a[pl][0] = v.x;
-                a[pl][1] = v.y;
-                a[pl][2] = v.z;
-                a[pl][3] = v.w;
-            }
+        };
+        for (int i = part * kLinThreads + threadIdx.x; i < ntok * (kOut / 4); i += p.split * kLinThreads) {
+            const int tok = i / (kOut / 4), f = 4 * (i % (kOut / 4)), n = f0 + f;
+            if (n >= p.N) continue;
+            float a[4], u[4];
+            total(tok * kFeat + f, a);
+            if (GLU) total(tok * kFeat + kOut + f, u);
             const int64_t t = t0 + tok;
             float o[4], res[4] = {0.f, 0.f, 0.f, 0.f};
             const bool full = n + 3 < p.N;
             if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + n, p.N - n, res);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float v = a[0][j];
+                float v = a[j];
                 if (p.bias && n + j < p.N) v += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + n + j));
                 if (GLU) {
-                    float u = a[kPlanes - 1][j];
-                    if (p.bias && n + j < p.N) u += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n + j));
-                    v = silu_fast(v) * u;
+                    if (p.bias && n + j < p.N)
+                        u[j] += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n + j));
+                    v = silu_fast(v) * u[j];
                 } else {
                     v = apply_act(p.act, v);
                 }
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_kernel(const __grid_consta
 
 template <bool F16, bool GLU>
 cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
-    constexpr int planes = GLU ? 2 : 1, max_nt = GLU ? 128 : 256;
+    constexpr int kOut = GLU ? kFeat / 2 : kFeat;
     LinKernelArgs p = {};
     p.T = a.T;
     p.N = a.N;
@@ -344,27 +344,43 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
     p.ctrl = a.ctrl;
     p.vec = vec4_ok(a.y, a.ldy, 2);
     p.vec_res = vec4_ok(a.res, a.ldr, a.res_f32 ? 4 : 2);
-    const int ttiles = (a.T + max_nt - 1) / max_nt;
+    // Tiles of at most 128 tokens (one of up to 160 where that is all of them): tensor memory
+    // and shared memory then let two CTAs share an SM.  Stages: four, or as many as that
+    // leaves room for.
+    const int ttiles = a.T <= 160 ? 1 : (a.T + 127) / 128;
     p.nt = ((a.T + ttiles - 1) / ttiles + 15) & ~15;
     p.tmem_cols = 32;
-    while ((int)p.tmem_cols < planes * p.nt) p.tmem_cols *= 2;
-    p.ftiles = (a.N + kFeat - 1) / kFeat;
+    while ((int)p.tmem_cols < p.nt) p.tmem_cols *= 2;
+    p.ftiles = (a.N + kOut - 1) / kOut;
     const int chunks = (a.K + kBK - 1) / kBK;
     const int64_t tiles = (int64_t)p.ftiles * ttiles;
-    p.split = 1;
-    while (p.split < 8 && tiles * p.split < 148 && p.split * 4 <= chunks) p.split *= 2;
-    const int per = (chunks + p.split - 1) / p.split;
-    const int stage_bytes = planes * kTileBytes + p.nt * kBK * 2;
-    const int sums_bytes = planes * p.nt * kFeat * 4;
-    p.stages = (200 * 1024) / stage_bytes;
-    if (p.stages > kMaxStages) p.stages = kMaxStages;
-    if (p.stages > per) p.stages = per;
-    size_t smem = (size_t)p.stages * stage_bytes;
-    if (smem < (size_t)sums_bytes) smem = sums_bytes;
-    if (smem < tmem_smem(p.tmem_cols)) smem = tmem_smem(p.tmem_cols);
-    smem += 1024;
+    const int stage_bytes = kTileBytes + p.nt * kBK * 2;
+    size_t smem = 0;
+    auto plan = [&](int split) {                        // -> CTAs that are resident at once
+        const int fit = p.nt <= 128 ? 112 * 1024 / stage_bytes : 4, per = (chunks + split - 1) / split;
+        p.split = split;
+        p.stages = fit < 4 ? fit : 4;
+        if (p.stages > per) p.stages = per;
+        smem = (size_t)p.stages * stage_bytes;
+        const size_t sums = (size_t)p.nt * kFeat * 4;
+        if (smem < sums) smem = sums;
+        if (smem < tmem_smem(p.tmem_cols)) smem = tmem_smem(p.tmem_cols);
+        smem += 1024;
+        return a.num_ctas * (int64_t)(228 * 1024 / (smem + 1024 + sizeof(LinShared)));
+    };
+    // K parts: as many as leave every CTA two stages or more of work and all CTAs resident at
+    // once, at most two on an SM (one token, 2048 -> 7168: 13.1 us with one part, 9.9 with
+    // two, 9.0 with four or five, 9.2 with six, 12.5 with eight, in a second wave).
+    plan(1);
+    for (int split = 2; split <= kMaxSplit && split * 2 <= chunks; ++split) {
+        const int64_t slots = plan(split);
+        if (tiles * split > slots || tiles * split > 2 * a.num_ctas) {
+            plan(split - 1);
+            break;
+        }
+    }
     CUtensorMap wm, xm;
-    if (!make_map(&wm, F16, a.w, (int64_t)planes * a.N, a.K, a.ldw, kFeat) ||
+    if (!make_map(&wm, F16, a.w, (int64_t)(GLU ? 2 : 1) * a.N, a.K, a.ldw, kOut) ||
         !make_map(&xm, F16, a.x, a.T, a.K, a.ldx, p.nt))
         return cudaErrorInvalidConfiguration;
     if (tiles * p.split > INT32_MAX) return cudaErrorInvalidConfiguration;
