@@ -138,13 +138,12 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _on(device):
-    """Context with `device` current (nothing to do when it already is)."""
-    import contextlib
+def _raw_stream(stream, device_index):
+    """The cudaStream_t of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return torch._C._cuda_getCurrentRawStream(device_index)
 
 
 # ---- packing (host) -----------------------------------------------------------
@@ -310,12 +309,21 @@ def moe_route_fixed(cfg, T, x, ids, gates, rt: dict, ws, stream=None) -> None:
 
 def moe_route_scored(cfg, router: Router, T, x, router_w, router_b, balance, rt: dict, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a balance bias (device float32 [E] or None)
-    that steers the choice only, expert groups and scaled weights."""
-    r = routing_struct(rt)
-    _check("moe_route_scored",
-           lib().moe_route_scored(ctypes.byref(_shape(cfg)), ctypes.byref(router), T, _ptr(x), _ptr(router_w),
-                                  _ptr(router_b), _ptr(balance), ctypes.byref(r), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)))
+    that steers the choice only, expert groups and scaled weights.  Runs on `stream` (default:
+    the current stream of x's device)."""
+    import torch
+    dev = x.get_device()
+    args = (ctypes.byref(Shape(cfg.H, cfg.I, cfg.E, cfg.k, cfg.S)), ctypes.byref(router), T, x.data_ptr(),
+            router_w.data_ptr(), None if router_b is None else router_b.data_ptr(),
+            None if balance is None else balance.data_ptr(), ctypes.byref(routing_struct(rt)), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if torch._C._cuda_getDevice() == dev:
+        st = lib().moe_route_scored(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = lib().moe_route_scored(*args)
+    if st != MOE_OK:
+        raise MoeError("moe_route_scored", st)
 
 
 def moe_gather_rows(src, index, divisor, dst, ws, n=None, stream=None) -> None:
@@ -333,15 +341,33 @@ def moe_combine_pairs(T, k, rows, inv_perm, gates, shared, y, ws, stream=None) -
                                                          ws.numel() * ws.element_size(), _stream(stream)))
 
 
-def _rows(name, t, shape, dtypes, device):
-    """Row stride of a matrix argument; raises ValueError unless it is a tensor of this
-    shape, one of these types, on this device, with adjacent elements in a row."""
-    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device:
-        raise ValueError(f"{name}: expected {shape} of {dtypes} on {device}, got {tuple(t.shape)} of {t.dtype} on "
-                         f"{t.device}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name}: the elements of a row must be adjacent, got strides {t.stride()}")
-    return t.stride(0)
+def _linear_misuse(x, w, y, ws, bias, residual, act):
+    """Names what is wrong with moe_linear's tensors (the call itself only tests that all is
+    well, in few operations: a call takes as long as a small product)."""
+    import torch
+    dt, dev = x.dtype, x.device
+    if dt not in (torch.bfloat16, torch.float16) or x.dim() != 2 or w.dim() != 2:
+        return "x and w must be bfloat16 or float16 matrices"
+    if not x.is_cuda or ws.device != dev:
+        return "x and ws must be on one CUDA device"
+    n_w = w.shape[0]
+    N = n_w // 2 if act == ACT_SWIGLU else n_w
+    if act == ACT_SWIGLU and n_w % 2:
+        return "ACT_SWIGLU needs an even number of weight rows"
+    want = [("x", x, tuple(x.shape), (dt,)), ("w", w, (n_w, x.shape[1]), (dt,)), ("y", y, (x.shape[0], N), (dt,))]
+    if residual is not None:
+        want.append(("residual", residual, (x.shape[0], N), (dt, torch.float32)))
+    if bias is not None:
+        want.append(("bias", bias, (n_w,), (dt,)))
+    for name, t, shape, types in want:
+        if tuple(t.shape) != shape or t.dtype not in types or t.device != dev:
+            return (f"{name}: expected {shape} of {types} on {dev}, got {tuple(t.shape)} of {t.dtype} on {t.device}")
+        if shape[-1] > 1 and t.stride(-1) != 1:
+            return f"{name}: the elements of a row must be adjacent, got strides {t.stride()}"
+    return None
+
+
+_dtype_codes = {}
 
 
 def moe_linear(x, w, y, ws, bias=None, residual=None, act=ACT_NONE, stream=None) -> None:
@@ -352,38 +378,47 @@ def moe_linear(x, w, y, ws, bias=None, residual=None, act=ACT_NONE, stream=None)
     (its control block records device errors).  Runs on `stream` (default: the current stream
     of x's device)."""
     import torch
-    dt, dev = x.dtype, x.device
-    if dt not in (torch.bfloat16, torch.float16) or x.dim() != 2 or w.dim() != 2:
-        raise ValueError("moe_linear: x and w must be bfloat16 or float16 matrices")
-    if not x.is_cuda or ws.device != dev:
-        raise ValueError("moe_linear: x and ws must be on one CUDA device")
-    T, K = x.shape
-    n_w = w.shape[0]
-    N = n_w // 2 if act == ACT_SWIGLU else n_w
-    if act == ACT_SWIGLU and n_w != 2 * N:
-        raise ValueError("moe_linear: ACT_SWIGLU needs an even number of weight rows")
-    # a row stride means nothing to a single row: any valid one will do
-    up = (max(K, 1) + 7) // 8 * 8
-    ldx = _rows("x", x, (T, K), (dt,), dev) if T > 1 else (_rows("x", x, (T, K), (dt,), dev), up)[1]
-    ldw = _rows("w", w, (n_w, K), (dt,), dev) if n_w > 1 else (_rows("w", w, (n_w, K), (dt,), dev), up)[1]
-    ldy = _rows("y", y, (T, N), (dt,), dev)
-    ldy = ldy if T > 1 else N
-    ldr, rt = 0, F32
-    if residual is not None:
-        ldr = _rows("residual", residual, (T, N), (dt, torch.float32), dev)
-        ldr = ldr if T > 1 else N
-        rt = F32 if residual.dtype == torch.float32 else (BF16 if dt == torch.bfloat16 else F16)
-    if bias is not None and (tuple(bias.shape) != (n_w,) or bias.dtype != dt or bias.device != dev
-                             or (n_w > 1 and bias.stride(0) != 1)):
-        raise ValueError(f"bias: expected ({n_w},) contiguous of {dt} on {dev}")
-    d = LinearDesc(K, N, BF16 if dt == torch.bfloat16 else F16, rt, act, ldx, ldw, ldr, ldy)
-    with _on(dev):
-        s = stream if stream is not None else torch.cuda.current_stream(dev)
-        st = lib().moe_linear(ctypes.byref(d), T, x.data_ptr(), w.data_ptr(),
-                              None if bias is None else bias.data_ptr(),
-                              None if residual is None else residual.data_ptr(), y.data_ptr(), ws.data_ptr(),
-                              ws.numel() * ws.element_size(), s.cuda_stream)
-    _check("moe_linear", st)
+    if not _dtype_codes:
+        _dtype_codes.update({torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
+    dt, dev = x.dtype, x.get_device()
+    code = _dtype_codes.get(dt, F32)
+    ok = code != F32 and dev >= 0 and x.dim() == 2 and w.dim() == 2 and y.dim() == 2
+    if ok:
+        (T, K), (n_w, kw), (ty, N) = x.shape, w.shape, y.shape
+        (ldx, sx), (ldw, sw), (ldy, sy) = x.stride(), w.stride(), y.stride()
+        ok = (kw == K and ty == T and n_w == (2 * N if act == ACT_SWIGLU else N) and w.dtype is dt and y.dtype is dt
+              and w.get_device() == dev and y.get_device() == dev and ws.get_device() == dev
+              and (K == 1 or (sx == 1 and sw == 1)) and (N == 1 or sy == 1))
+    ldr, rt, r_ptr, b_ptr = 0, F32, None, None
+    if ok and residual is not None:
+        rt = _dtype_codes.get(residual.dtype, -1)
+        ok = residual.shape == y.shape and rt in (code, F32) and residual.get_device() == dev
+        if ok:
+            ldr, sr = residual.stride()
+            ok = N == 1 or sr == 1
+            r_ptr = residual.data_ptr()
+            if T == 1:
+                ldr = N
+    if ok and bias is not None:
+        ok = (bias.dim() == 1 and bias.shape[0] == n_w and bias.dtype is dt and bias.get_device() == dev
+              and (n_w == 1 or bias.stride(0) == 1))
+        b_ptr = bias.data_ptr()
+    if not ok:
+        raise ValueError(f"moe_linear: {_linear_misuse(x, w, y, ws, bias, residual, act) or 'unsupported arguments'}")
+    if T == 1:                                  # a row stride means nothing to a single row: any valid one does
+        ldx, ldy = (K + 7) // 8 * 8, N
+    if n_w == 1:
+        ldw = (K + 7) // 8 * 8
+    d = LinearDesc(K, N, code, rt, act, ldx, ldw, ldr, ldy)
+    args = (ctypes.byref(d), T, x.data_ptr(), w.data_ptr(), b_ptr, r_ptr, y.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size(), _raw_stream(stream, dev))
+    if torch._C._cuda_getDevice() == dev:
+        st = lib().moe_linear(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = lib().moe_linear(*args)
+    if st != MOE_OK:
+        raise MoeError("moe_linear", st)
 
 
 def moe_get_error(ws, stream=None):
