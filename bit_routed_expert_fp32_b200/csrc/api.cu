@@ -67,6 +67,11 @@ Ws ws_layout(const moe_shape* s, int64_t T) {
         yfl = yfl > need_dn ? yfl : need_dn;
         yfl = yfl > need_gu ? yfl : need_gu;
     }
+    // the scored router's weight planes lie there before the expert passes write it
+    if (T > kSmallT) {
+        const size_t planes = (size_t)(3 * E * H) / 2;
+        yfl = yfl > planes ? yfl : planes;
+    }
     w.ypart = off;
     off = align256(off + 4 * yfl);
     w.total = off;
@@ -190,6 +195,7 @@ static RouteArgs route_args(const moe_shape* shape, int32_t T, const uint16_t* d
     a.ops = T <= kSmallT;                                 // the decode operands (the decode
                                                           // path forms them itself above)
     a.iq = T <= kFusedMaxT ? ws + w.iq : nullptr;         // and the integer records
+    a.planes = reinterpret_cast<uint16_t*>(ws + w.ypart);
     a.ctrl = reinterpret_cast<Ctrl*>(ws + w.ctrl);
     a.r = *out;
     return a;

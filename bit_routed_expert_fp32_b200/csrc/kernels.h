@@ -24,6 +24,7 @@ struct RouteArgs {
     int ops;            // form the decode operands (Z tables, integer operands) here
     const int32_t* fixed_ids;   // moe_route_fixed: the caller's expert ids [T][k] (else null)
     const float* fixed_w;       // moe_route_fixed: the caller's gates [T][k]
+    uint16_t* planes;           // ws: the scored router's bf16 planes [3][E][H] (in ypart; T > kSmallT)
     Ctrl* ctrl;
     moe_routing r;
 };
@@ -180,10 +181,8 @@ inline size_t fused_ypart_floats(const moe_shape* s, int64_t T) {
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
-// pieces of it for more than kSmallT tokens: the logits, and the permutation from the
-// per-chunk bases that the top-k kernel leaves in a.hist
+// its logits for more than kSmallT tokens
 cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t s);
-cudaError_t launch_route_scatter(const RouteArgs& a, cudaStream_t s);
 // the scored router (route_scored.cu): how a token's scores choose its experts
 struct ScoreArgs {
     int sigmoid, n_groups, top_groups, group_top, renormalise;

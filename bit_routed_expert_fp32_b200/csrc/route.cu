@@ -509,11 +509,6 @@ cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_route_scatter(const RouteArgs& a, cudaStream_t s) {
-    route_scatter_kernel<<<(a.T + kChunk - 1) / kChunk, 32, 0, s>>>(a);
-    return cudaGetLastError();
-}
-
 cudaError_t launch_route_fixed(const RouteArgs& a, cudaStream_t s) {
     if (a.ops) {
         const int zwarps = a.T * 8 * ((a.H / 64 + 7) / 8);
@@ -539,7 +534,8 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
     const cudaError_t err = launch_route_logits(a, s);
     if (err != cudaSuccess) return err;
     route_topk_kernel<<<(a.T + kChunk - 1) / kChunk, 256, 0, s>>>(a);
-    return launch_route_scatter(a, s);
+    route_scatter_kernel<<<(a.T + kChunk - 1) / kChunk, 32, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -26,15 +26,21 @@ __device__ inline unsigned long long score_key(double c) {
     return (b >> 63) ? ~b : (b | (1ull << 63));
 }
 
-// One token's choice by one warp: lane l holds experts 8l .. 8l+7.  `scratch` (256 doubles of
-// this warp) serves the group scores.  Each round takes the largest key over the warp in two
-// 32-bit reductions (high words, then the low words of those that tie), the lowest lane and
-// the lowest expert inside it first.  Writes ids and weights of slots < k.
-__device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row, double* scratch, int lane,
-                              int32_t* ids_out, float* w_out, int32_t* s_ids) {
-    float L[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) L[j] = 8 * lane + j < E ? ldcg_f32(row + 8 * lane + j) : -INFINITY;
+// Scratch of a warp that chooses: its token's logits (and the fast path's values for groups
+// that do not align with lanes), or the careful path's values.
+union Scratch {
+    struct {
+        float L[256], c[256];
+    } f;
+    double d[256];
+};
+
+// One token's choice by one warp, in fp64 throughout: lane l holds experts 8l .. 8l+7 (L, -inf
+// past the last).  Each round takes the largest key over the warp in two 32-bit reductions
+// (high words, then the low words of those that tie), the lowest lane and the lowest expert
+// inside it first.  Leaves id and score of slot n in lane n < k.
+__device__ __noinline__ void choose_careful(const ScoreArgs& r, int E, int k, const float (&L)[8], Scratch& scratch,
+                                            int lane, int& my_id, double& my_s) {
     double s[8];
     if (r.sigmoid) {
 #pragma unroll
@@ -58,6 +64,7 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
     }
     unsigned long long key[8];
     const bool grouped = r.top_groups < r.n_groups;
+    __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int e = 8 * lane + j;
@@ -65,7 +72,7 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
         if (e < E) {
             const double c = r.balance ? s[j] + (double)__ldg(r.balance + e) : s[j];
             key[j] = score_key(c);
-            if (grouped) scratch[e] = c == c ? c : -INFINITY;
+            if (grouped) scratch.d[e] = c == c ? c : -INFINITY;
         }
     }
     if (grouped) {
@@ -77,7 +84,7 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
             double t1 = -INFINITY, t2 = -INFINITY;
             int i = lane % gs;
             for (int n = 0; n < gs; ++n) {
-                const double c = scratch[lane * gs + i];
+                const double c = scratch.d[lane * gs + i];
                 if (c > t1) {
                     t2 = t1;
                     t1 = c;
@@ -100,8 +107,6 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
         for (int j = 0; j < 8; ++j)
             if (8 * lane + j < E && !((kept >> ((8 * lane + j) / gs)) & 1u)) key[j] = 0;
     }
-    double my_s = 0.0;
-    int my_id = 0;
     for (int n = 0; n < k; ++n) {
         unsigned long long bk = key[0];
         int bj = 0;
@@ -131,7 +136,194 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
                 if (j == wj) key[j] = 0;
         }
     }
-    double w = lane < k ? my_s : 0.0;
+}
+
+// Order-preserving 32-bit key of a value that is not NaN (0 is below every key) and back.
+__device__ inline uint32_t key32(float f) {
+    const uint32_t b = __float_as_uint(f + 0.f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ inline float unkey32(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
+
+// The choice in fp32 where fp32 decides it.  Scores from the fast exponential are off by less
+// than 1e-6 (its documented error of 2 + 1.17 |x| ulp counts in proportion to s (1 - s), or
+// to p); adding the balance rounds once more.  So where neighbours among the k + 1 largest
+// values (and the group scores beside the border) lie further apart than both can be off,
+// their order is the exact one; otherwise, and where NaN or infinities meet, false is
+// returned and the careful path decides.  A softmax without balance has the order of its
+// logits (as long as fp64 scores would not vanish).  A key gives its low three bits to the
+// expert's place in the lane; a lane's eight are sorted once and then only popped.
+__device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, const float (&L)[8], const float (&b)[8],
+                                            Scratch& scratch, int lane, int& my_id) {
+    constexpr float kAbs = 4e-6f, kRel = 1.2e-6f;         // kRel: the rounding, and eight steps of a key
+    const bool grouped = r.top_groups < r.n_groups, by_logit = !r.sigmoid && !r.balance;
+    float c[8], m = 0.f;
+    if (r.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c[j] = __fdividef(1.f, 1.f + __expf(-L[j])) + b[j];
+    } else {
+        m = L[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = fmaxf(m, L[j]);
+        m = unkey32(__reduce_max_sync(0xffffffffu, m == m ? key32(m) : 0u));
+        if (!by_logit || grouped) {
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                c[j] = __expf(L[j] - m);
+                z += c[j];
+            }
+            z = warp_sum(z);
+            const float iz = __fdividef(1.f, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) c[j] = c[j] * iz + b[j];
+        }
+    }
+    bool fine = true;
+    uint32_t key[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const bool in = 8 * lane + j < E;
+        const float v = by_logit ? L[j] : c[j];
+        fine &= !in || v == v;
+        if (grouped) fine &= !in || c[j] == c[j];
+        key[j] = in ? (key32(v) & ~7u) | (7u - j) : 0u;
+    }
+    if (!__all_sync(0xffffffffu, fine)) return false;
+    if (grouped) {
+        const int gs = E / r.n_groups, lpg = gs >> 3;
+        float t1, t2;
+        int leader;                                       // lanes apart that groups lie
+        if ((gs & 7) == 0 && (lpg & (lpg - 1)) == 0) {
+            // a group is a power of two of lanes: top two of eight, then across them
+            t1 = fmaxf(c[0], c[1]);
+            t2 = fminf(c[0], c[1]);
+#pragma unroll
+            for (int j = 2; j < 8; ++j) {
+                t2 = fmaxf(t2, fminf(t1, c[j]));
+                t1 = fmaxf(t1, c[j]);
+            }
+            for (int o = 1; o < lpg; o <<= 1) {
+                const float a1 = __shfl_xor_sync(0xffffffffu, t1, o), a2 = __shfl_xor_sync(0xffffffffu, t2, o);
+                t2 = fmaxf(fminf(t1, a1), fmaxf(t2, a2));
+                t1 = fmaxf(t1, a1);
+            }
+            leader = lpg;
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) scratch.f.c[8 * lane + j] = c[j];
+            __syncwarp();
+            t1 = t2 = -INFINITY;
+            if (lane < r.n_groups) {
+                int i = lane % gs;
+                for (int n = 0; n < gs; ++n) {
+                    const float v = scratch.f.c[lane * gs + i];
+                    t2 = fmaxf(t2, fminf(t1, v));
+                    t1 = fmaxf(t1, v);
+                    if (++i == gs) i = 0;
+                }
+            }
+            leader = 1;
+        }
+        const float sc = r.group_top == 2 ? t1 + t2 : t1;
+        const int mine = lane / leader;
+        int rank = 0;
+        for (int g = 0; g < r.n_groups; ++g) {
+            const float o = __shfl_sync(0xffffffffu, sc, g * leader);
+            rank += o > sc || (o == sc && g < mine);
+        }
+        const bool in = mine < r.n_groups, keep = in && rank < r.top_groups;
+        const unsigned lanes = __ballot_sync(0xffffffffu, keep);
+        const float lo = unkey32(__reduce_min_sync(0xffffffffu, keep && sc == sc ? key32(sc) : 0xFF800000u));
+        const float hi = unkey32(__reduce_max_sync(0xffffffffu, in && !keep ? key32(sc) : 0x007FFFFFu));
+        if (__any_sync(0xffffffffu, in && sc != sc) || !(lo - hi > 2.f * kAbs + 2.f * kRel * (fabsf(lo) + fabsf(hi))))
+            return false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int g = leader == 1 ? (8 * lane + j) / gs : mine;
+            if (!((lanes >> (g * leader)) & 1u)) key[j] = 0;
+        }
+    }
+    // descending, by the 19 comparators of Batcher's odd-even merge sort
+#pragma unroll
+    for (int q = 0; q < 19; ++q) {
+        constexpr int A[19] = {0, 2, 4, 6, 0, 1, 4, 5, 1, 5, 0, 1, 2, 3, 2, 3, 1, 3, 5};
+        constexpr int B[19] = {1, 3, 5, 7, 2, 3, 6, 7, 2, 6, 4, 5, 6, 7, 4, 5, 2, 4, 6};
+        const uint32_t x = key[A[q]], y = key[B[q]];
+        key[A[q]] = max(x, y);
+        key[B[q]] = min(x, y);
+    }
+    uint32_t mine = 0;                                     // lane n: the n-th largest key
+    for (int n = 0; n <= k; ++n) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+        const int wl = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
+        if (lane == wl) {
+#pragma unroll
+            for (int j = 0; j < 7; ++j) key[j] = key[j + 1];
+            key[7] = 0;
+        }
+        if (lane == n) {
+            mine = top;
+            my_id = 8 * wl + 7 - (int)(top & 7u);
+        }
+    }
+    const float v = unkey32(mine & ~7u);
+    const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
+    bool ok = true;
+    if (lane < k) {
+        const float w = unkey32(next & ~7u);
+        ok = next == 0 || v - w > (by_logit ? 0.f : kAbs) + kRel * (fabsf(v) + fabsf(w));
+        if (by_logit) ok &= v - m > -700.f;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// One token: choice, weights, output of slots < k.  b: the lane's eight balance values.
+__device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row, const float (&b)[8], Scratch& scratch,
+                              int lane, int32_t* ids_out, float* w_out, int32_t* s_ids) {
+    float L[8];
+    if ((E & 3) == 0 && 8 * lane + 8 <= E) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(row) + 2 * lane);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(row) + 2 * lane + 1);
+        L[0] = u.x; L[1] = u.y; L[2] = u.z; L[3] = u.w;
+        L[4] = v.x; L[5] = v.y; L[6] = v.z; L[7] = v.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) L[j] = 8 * lane + j < E ? ldcg_f32(row + 8 * lane + j) : -INFINITY;
+    }
+    int my_id = 0;
+    double s = 0.0;
+    __syncwarp();
+    if (choose_fast(r, E, k, L, b, scratch, lane, my_id)) {
+        // the chosen scores in fp64, one a lane; softmax scores relative to the largest logit,
+        // over the sum of all only where they are not renormalised
+        __syncwarp();
+        *reinterpret_cast<float4*>(scratch.f.L + 8 * lane) = make_float4(L[0], L[1], L[2], L[3]);
+        *reinterpret_cast<float4*>(scratch.f.L + 8 * lane + 4) = make_float4(L[4], L[5], L[6], L[7]);
+        __syncwarp();
+        const double l = lane < k ? (double)scratch.f.L[my_id] : 0.0;
+        if (r.sigmoid) {
+            s = 1.0 / (1.0 + exp(-l));
+        } else {
+            float m = L[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) m = fmaxf(m, L[j]);
+            m = unkey32(__reduce_max_sync(0xffffffffu, key32(m)));
+            s = exp(l - (double)m);
+            if (!r.renormalise) {
+                double z = 0.0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z += exp((double)L[j] - (double)m);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) z += shfl_xor_d(z, o);
+                s /= z;
+            }
+        }
+    } else {
+        choose_careful(r, E, k, L, scratch, lane, my_id, s);
+    }
+    double w = lane < k ? s : 0.0;
     if (r.renormalise) {
         double sum = w;
 #pragma unroll
@@ -143,6 +335,12 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
         w_out[lane] = (float)(w * (double)r.scale);
         if (s_ids) s_ids[lane] = my_id;
     }
+}
+
+// The lane's eight balance values (0 without one).
+__device__ inline void load_balance(const ScoreArgs& r, int E, int lane, float (&b)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = r.balance && 8 * lane + j < E ? __ldg(r.balance + 8 * lane + j) : 0.f;
 }
 
 // ---------------------------------------------------------------- up to kSmallT tokens
@@ -160,7 +358,7 @@ template <int NTL>   // 8-token MMA columns
 struct SmallSmem {
     union {
         float part[kSmWarps][kSmExperts][8 * NTL];
-        double scratch[kSmWarps][256];
+        Scratch scratch[kSmWarps];
     };
     Df sum[kSmExperts][8 * NTL];
     int32_t ids[kSmallT * 16];
@@ -282,8 +480,10 @@ __global__ void __launch_bounds__(kSmThreads) scored_small_kernel(RouteArgs p, S
     __threadfence();
 
     for (int i = threadIdx.x; i < 256; i += kSmThreads) S.cnt[i] = 0;
+    float bal[8];
+    load_balance(r, p.E, lane, bal);
     for (int t = warp; t < p.T; t += kSmWarps)
-        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, S.scratch[warp], lane, p.r.topk_ids + (size_t)t * p.k,
+        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, S.scratch[warp], lane, p.r.topk_ids + (size_t)t * p.k,
                       p.r.topk_w + (size_t)t * p.k, S.ids + t * p.k);
     __syncthreads();
     for (int i = threadIdx.x; i < p.T * p.k; i += kSmThreads) atomicAdd(&S.cnt[S.ids[i]], 1);
@@ -306,36 +506,115 @@ __global__ void __launch_bounds__(kSmThreads) scored_small_kernel(RouteArgs p, S
 }
 
 // ---------------------------------------------------------------- above kSmallT tokens
-// One CTA per chunk of tokens, a warp per token; the last CTA scans the chunks' histograms.
-__global__ void __launch_bounds__(256) scored_topk_kernel(RouteArgs p, ScoreArgs r) {
-    __shared__ double s_scratch[8][256];
+// The router's rows as three bf16 planes [3][E][H] (w = w1 + w2 + w3 exactly, each the
+// rounding of what is left), for the logits kernel's operand loads; zeroes the histograms
+// that the top-k kernel adds to.
+__global__ void __launch_bounds__(256) scored_split_kernel(RouteArgs p, uint16_t* planes, int32_t* sums, int n_sums) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const size_t n8 = (size_t)p.E * p.H / 8, plane = (size_t)p.E * p.H;
+    const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
+    for (size_t i = i0; i < (size_t)n_sums; i += step) sums[i] = 0;
+    const size_t n_hist = (size_t)((p.T + kChunk - 1) / kChunk) * p.E;
+    for (size_t i = i0; i < n_hist; i += step) p.hist[i] = 0;
+    for (size_t i = i0; i < n8; i += step) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p.Wr) + 2 * i);
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p.Wr) + 2 * i + 1);
+        float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int pl = 0; pl < 3; ++pl) {
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float u = bf16_part(w[2 * q]), v = bf16_part(w[2 * q + 1]);
+                o[q] = pack_bf16x2(u, v);
+                w[2 * q] -= u;
+                w[2 * q + 1] -= v;
+            }
+            *reinterpret_cast<uint4*>(planes + pl * plane + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// Top-k: a warp per token.  Adds to the histograms of the token's chunk (p.hist) and of its
+// span of kSpan chunks (integer atomics: the sums do not depend on their order), from which
+// the scatter kernel's CTAs form their bases by themselves.
+constexpr int kTopWarps = 8, kSpan = 16;
+
+__global__ void __launch_bounds__(32 * kTopWarps, 3) scored_topk_kernel(RouteArgs p, ScoreArgs r, int32_t* sums) {
+    __shared__ Scratch s_scratch[kTopWarps];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float bal[8];
+    load_balance(r, p.E, lane, bal);
+    for (int t = blockIdx.x * kTopWarps + warp; t < p.T; t += gridDim.x * kTopWarps) {
+        const int c = t / kChunk;
+        int32_t* ids = p.r.topk_ids + (size_t)t * p.k;
+        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, s_scratch[warp], lane, ids,
+                      p.r.topk_w + (size_t)t * p.k, nullptr);
+        if (lane < p.k) {
+            const int e = ids[lane];                           // the lane's own write
+            atomicAdd(p.hist + (size_t)c * p.E + e, 1);
+            atomicAdd(sums + (size_t)(c / kSpan) * p.E + e, 1);
+        }
+    }
+}
+
+// Permutation: one CTA per chunk.  Thread e adds up its expert's rows in the spans and chunks
+// before this one and, over all spans, its total; the warps then take a contiguous share of
+// the chunk's pairs each, count it, and rank its pairs from where the warps before end.
+__global__ void __launch_bounds__(256) scored_scatter_kernel(RouteArgs p, const int32_t* sums) {
     __shared__ int s_cnt[256];
     __shared__ int s_off[257];
-    __shared__ int s_last;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x;
-    if (c == 0 && threadIdx.x == 0) {                   // no expert pass of this workspace runs now
-        p.ctrl->work[0] = 0;
+    __shared__ int s_run[8][256];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
+    const int c = blockIdx.x, span = c / kSpan, n_spans = ((int)gridDim.x + kSpan - 1) / kSpan;
+    int base = 0, total = 0;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int q = 0; q < n_spans; ++q) {
+            const int v = __ldcg(sums + (size_t)q * p.E + e);
+            total += v;
+            if (q < span) base += v;
+        }
+#pragma unroll 8
+        for (int q = span * kSpan; q < c; ++q) base += __ldcg(p.hist + (size_t)q * p.E + e);
+    }
+    s_cnt[e] = total;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s_run[w][e] = 0;
+    __syncthreads();
+    const int t0 = c * kChunk, pair0 = t0 * p.k, n = (min(p.T, t0 + kChunk) - t0) * p.k;
+    const int share = (n + 255) / 256 * 32, b0 = min(n, warp * share), b1 = min(n, b0 + share);
+    const int32_t* ids = p.r.topk_ids + pair0;
+    for (int i = b0 + lane; i < b1; i += 32) atomicAdd(&s_run[warp][ids[i]], 1);
+    if (warp == 0) warp_scan_counts(s_cnt, s_off, p.E, lane);
+    __syncthreads();
+    if (e < p.E) {
+        int run = s_off[e] + base;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const int v = s_run[w][e];
+            s_run[w][e] = run;
+            run += v;
+        }
+    }
+    __syncthreads();
+    warp_scatter(ids + b0, pair0 + b0, b1 - b0, s_run[warp], p.r.perm, p.r.inv_perm, lane, p.E);
+    if (c != 0) return;
+    if (e < p.E) {
+        p.r.counts[e] = total;
+        p.r.offsets[e] = s_off[e];
+    }
+    if (e == 0) {
+        p.r.offsets[p.E] = s_off[p.E];
+        p.ctrl->work[0] = 0;                              // no expert pass of this workspace runs now
         p.ctrl->work[1] = 0;
     }
-    for (int i = threadIdx.x; i < 256; i += blockDim.x) s_cnt[i] = 0;
-    __syncthreads();
-    const int tend = min(p.T, (c + 1) * kChunk);
-    for (int t = c * kChunk + warp; t < tend; t += 8) {
-        int32_t* ids = p.r.topk_ids + (size_t)t * p.k;
-        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, s_scratch[warp], lane, ids, p.r.topk_w + (size_t)t * p.k,
-                      nullptr);
-        if (lane < p.k) atomicAdd(&s_cnt[ids[lane]], 1);       // the lane's own write
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(size_t)c * p.E + e] = s_cnt[e];
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(&p.ctrl->topk_ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    chunk_scan(p, s_cnt, s_off, gridDim.x);
+    if (warp == 1) warp_active(s_cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
 }
 
 template <int NTL>
@@ -370,10 +649,17 @@ cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, cudaStre
         if (a.T <= 32) return launch_small<4>(a, r, s);
         return launch_small<8>(a, r, s);
     }
-    const cudaError_t err = launch_route_logits(a, s);
+    // the spans' sums and the planes take regions of the workspace that only moe_forward uses
+    const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
+    int32_t* sums = reinterpret_cast<int32_t*>(a.zx);
+    cudaError_t err = launch_pdl(scored_split_kernel, dim3(4 * 148), dim3(256), 0, s, a, a.planes, sums, n_sums);
     if (err != cudaSuccess) return err;
-    scored_topk_kernel<<<(a.T + kChunk - 1) / kChunk, 256, 0, s>>>(a, r);
-    return launch_route_scatter(a, s);
+    if ((err = launch_route_logits(a, s)) != cudaSuccess) return err;
+    int top = (a.T + kTopWarps - 1) / kTopWarps;
+    if (top > 6 * 148) top = 6 * 148;
+    if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
+        return err;
+    return launch_pdl(scored_scatter_kernel, dim3(nchunks), dim3(256), 0, s, a, (const int32_t*)sums);
 }
 
 }  // namespace moe
