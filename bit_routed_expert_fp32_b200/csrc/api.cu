@@ -293,7 +293,7 @@ moe_status moe_route_scored(const moe_shape* shape, const moe_router* router, in
     const RouteArgs a = route_args(shape, T, d_x, d_router_w, d_router_b, out, d_ws);
     const ScoreArgs r = {router->score == MOE_SCORE_SIGMOID, G,
                          router->top_groups, router->group_top, router->renormalise, router->scale, d_balance};
-    return launch_route_scored(a, r, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_route_scored(a, r, sm_count(), static_cast<cudaStream_t>(stream)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 moe_status moe_route_fixed(const moe_shape* shape, int32_t T, const uint16_t* d_x, const int32_t* d_ids,

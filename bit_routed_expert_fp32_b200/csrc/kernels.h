@@ -181,15 +181,15 @@ inline size_t fused_ypart_floats(const moe_shape* s, int64_t T) {
 }
 
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t s);
-// its logits for more than kSmallT tokens
-cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t s);
 // the scored router (route_scored.cu): how a token's scores choose its experts
 struct ScoreArgs {
     int sigmoid, n_groups, top_groups, group_top, renormalise;
     float scale;
     const float* balance;    // [E] or null: added to the scores for the choice only
 };
-cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, cudaStream_t s);
+cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_ctas, cudaStream_t s);
+// its logits above kSmallT tokens, from the planes in a.planes (scored_logits.cu)
+cudaError_t launch_scored_logits(const RouteArgs& a, int num_ctas, cudaStream_t s);
 // the decode operands (Z tables) of a.T tokens, for the decode path above kSmallT tokens
 cudaError_t launch_decode_operands(const RouteArgs& a, cudaStream_t s);
 // the routing of caller-given expert ids and gates (a.fixed_ids): histogram, scan,

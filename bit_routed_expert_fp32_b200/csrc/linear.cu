@@ -136,17 +136,6 @@ struct LinShared {
     int abort_flag;
 };
 
-__device__ inline int ld_volatile(const int& v) { return *reinterpret_cast<const volatile int*>(&v); }
-__device__ inline void st_volatile(int& v, int x) { *reinterpret_cast<volatile int*>(&v) = x; }
-
-__device__ inline bool wait_or_flag(LinShared& S, uint64_t* bar, uint32_t parity, Ctrl* ctrl, uint32_t detail) {
-    if (ld_volatile(S.abort_flag)) return false;
-    if (mbar_wait_bounded(bar, parity, kWaitLimit)) return true;
-    st_volatile(S.abort_flag, 1);
-    report_error(ctrl, MOE_ERR_TIMEOUT, detail);
-    return false;
-}
-
 template <bool F16, bool GLU>
 __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_constant__ LinKernelArgs p,
                                                              const __grid_constant__ CUtensorMap wmap,
@@ -190,7 +179,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         for (int i = 0; i < n_stage; ++i) {
             const int s = i % p.stages;
             const uint32_t par = ((uint32_t)(i / p.stages) & 1) ^ 1;
-            if (!mbar_try_wait(&S.empty_[s], par)) wait_or_flag(S, &S.empty_[s], par, p.ctrl, kDetWaitEmpty | 0x60);
+            if (!mbar_try_wait(&S.empty_[s], par)) wait_or_flag(S.abort_flag, &S.empty_[s], par, p.ctrl, kDetWaitEmpty | 0x60);
             __syncwarp();
             if (ld_volatile(S.abort_flag)) break;
             if (elect_one()) {
@@ -218,10 +207,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         bool ok = true;
         const uint32_t stall = p.ctrl->test_stall;
         if (stall) {
-            // failure-path tests: a bounded wait on a barrier that nothing completes
-            bool got = false;
-            if (lane == 0) got = mbar_wait_bounded(&S.stall_bar, 0, stall);
-            if (!__shfl_sync(0xffffffffu, got, 0)) {
+            if (test_stall(&S.stall_bar, stall, lane)) {
                 if (lane == 0) {
                     st_volatile(S.abort_flag, 1);
                     report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetTestStall | 0x60);
@@ -233,7 +219,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         for (int i = 0; i < n_stage && ok; ++i) {
             const int s = i % p.stages;
             const uint32_t par = (uint32_t)(i / p.stages) & 1;
-            if (!mbar_try_wait(&S.full[s], par)) ok = wait_or_flag(S, &S.full[s], par, p.ctrl, kDetWaitFull | 0x60);
+            if (!mbar_try_wait(&S.full[s], par)) ok = wait_or_flag(S.abort_flag, &S.full[s], par, p.ctrl, kDetWaitFull | 0x60);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             if (ok && elect_one()) {
@@ -438,23 +424,6 @@ struct PairShared {
     int abort_flag;
 };
 
-// Bounded wait that gives up at once when either CTA of the pair has given up.
-__device__ inline bool pair_wait(PairShared& S, uint64_t* bar, uint32_t parity, Ctrl* ctrl, uint32_t detail) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    while (!ld_volatile(S.abort_flag)) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (clock64() - t0 > kWaitLimit) {
-            st_volatile(S.abort_flag, 1);
-            st_peer_u32(map_peer(smem_u32(&S.abort_flag), cluster_rank() ^ 1), 1);
-            report_error(ctrl, MOE_ERR_TIMEOUT, detail);
-        }
-    }
-    return false;
-}
-
 __device__ inline void pair_tile(const PairArgs& p, int tile, int& tt, int& ft) {
     const int per = p.group * p.ftiles, g = tile / per, r = tile - g * per;
     const int rows = min(p.group, p.ttiles - g * p.group);
@@ -511,7 +480,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int trow = tt * kPairTok + rank * 128;
             const int wrow = GLU ? rank * p.N + ft * kOut : ft * kOut + rank * 128;
             for (int kc = 0; kc < chunks; ++kc) {
-                if (!__all_sync(0xffffffffu, pair_wait(S, &S.empty_[slot], par, p.ctrl, kDetWaitEmpty | 0x62))) {
+                if (!__all_sync(0xffffffffu, pair_wait(S.abort_flag, &S.empty_[slot], par, p.ctrl, kDetWaitEmpty | 0x62))) {
                     stop = true;
                     break;
                 }
@@ -530,24 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
             }
         }
-        // after an abort no copy may still target either CTA's shared memory at exit: the
-        // leader, on whose barriers the bytes of both count, waits (bounded) for the last
-        // phase issued on every slot; the other CTA, which may have issued past the leader,
-        // gives its last copies (microseconds) some half a millisecond
-        if (stop && lane == 0) {
-            if (rank == 0) {
-                for (int d = 0; d < kPairStages && d < issued; ++d) {
-                    const int i = issued - 1 - d;
-                    if (!mbar_wait_bounded(&S.full[i % kPairStages], (uint32_t)(i / kPairStages) & 1, kWaitLimit)) {
-                        report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetDrain | 0x62);
-                        break;
-                    }
-                }
-            } else {
-                const long long c0 = clock64();
-                while (clock64() - c0 < 1000000) __nanosleep(1000);
-            }
-        }
+        if (stop && lane == 0) pair_drain(S.full, kPairStages, issued, rank == 0, p.ctrl, kDetDrain | 0x62);
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         // ---- MMA issuer (the leader's) ----------------------------------------------------
@@ -556,14 +508,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const uint32_t stall = p.ctrl->test_stall;
         bool ok = true;
         if (stall) {
-            // failure-path tests: a bounded wait on a barrier that nothing completes
-            bool got = false;
-            if (lane == 0) got = mbar_wait_bounded(&S.stall_bar, 0, stall);
-            if (!__shfl_sync(0xffffffffu, got, 0)) {
+            if (test_stall(&S.stall_bar, stall, lane)) {
                 if (lane == 0) {
                     report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetTestStall | 0x62);
-                    st_volatile(S.abort_flag, 1);
-                    st_peer_u32(map_peer(smem_u32(&S.abort_flag), 1), 1);
+                    pair_abort(S.abort_flag);
                 }
                 ok = false;
             }
@@ -573,11 +521,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         uint32_t par = 0;
         for (int tile = pair; tile < n_tiles && ok; tile += n_pairs, ++n) {
             const int buf = n & 1;
-            ok = pair_wait(S, &S.acc_empty[buf], (uint32_t)((n >> 1) & 1) ^ 1, p.ctrl, kDetWaitEmpty | 0x63);
+            ok = pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((n >> 1) & 1) ^ 1, p.ctrl, kDetWaitEmpty | 0x63);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             for (int kc = 0; kc < chunks && ok; ++kc) {
-                ok = pair_wait(S, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x62);
+                ok = pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x62);
                 ok = __all_sync(0xffffffffu, ok);
                 fence_after();
                 if (ok && elect_one()) {
@@ -633,7 +581,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             };
             if (whole && p.res) load_res(0);
             if (!__all_sync(0xffffffffu,
-                            pair_wait(S, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
+                            pair_wait(S.abort_flag, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
                 break;
             fence_after();
             const uint32_t tl = tmem + buf * 256 + half * kCols + ((uint32_t)(32 * q) << 16);

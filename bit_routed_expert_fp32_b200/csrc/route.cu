@@ -501,14 +501,6 @@ cudaError_t launch_decode_operands(const RouteArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_route_logits(const RouteArgs& a, cudaStream_t s) {
-    const cudaError_t err = set_smem_limit(route_logits_mma_kernel, kRouteMmaSmem);
-    if (err != cudaSuccess) return err;
-    dim3 g1((a.T + RBM - 1) / RBM, (a.E + RBN - 1) / RBN);
-    route_logits_mma_kernel<<<g1, 256, kRouteMmaSmem, s>>>(a);
-    return cudaGetLastError();
-}
-
 cudaError_t launch_route_fixed(const RouteArgs& a, cudaStream_t s) {
     if (a.ops) {
         const int zwarps = a.T * 8 * ((a.H / 64 + 7) / 8);
@@ -531,8 +523,10 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t s) {
         const int zwarps = a.T * 8 * ((a.H / 64 + 7) / 8);
         route_xz_kernel<<<(zwarps + 7) / 8, 256, 0, s>>>(a);
     }
-    const cudaError_t err = launch_route_logits(a, s);
+    const cudaError_t err = set_smem_limit(route_logits_mma_kernel, kRouteMmaSmem);
     if (err != cudaSuccess) return err;
+    dim3 g1((a.T + RBM - 1) / RBM, (a.E + RBN - 1) / RBN);
+    route_logits_mma_kernel<<<g1, 256, kRouteMmaSmem, s>>>(a);
     route_topk_kernel<<<(a.T + kChunk - 1) / kChunk, 256, 0, s>>>(a);
     route_scatter_kernel<<<(a.T + kChunk - 1) / kChunk, 32, 0, s>>>(a);
     return cudaGetLastError();

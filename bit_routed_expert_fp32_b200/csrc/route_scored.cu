@@ -642,7 +642,7 @@ cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, cudaStream_t s) {
+cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_ctas, cudaStream_t s) {
     if (a.T <= kSmallT) {
         if (a.T <= 8) return launch_small<1>(a, r, s);
         if (a.T <= 16) return launch_small<2>(a, r, s);
@@ -652,11 +652,11 @@ cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, cudaStre
     // the spans' sums and the planes take regions of the workspace that only moe_forward uses
     const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
     int32_t* sums = reinterpret_cast<int32_t*>(a.zx);
-    cudaError_t err = launch_pdl(scored_split_kernel, dim3(4 * 148), dim3(256), 0, s, a, a.planes, sums, n_sums);
+    cudaError_t err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
     if (err != cudaSuccess) return err;
-    if ((err = launch_route_logits(a, s)) != cudaSuccess) return err;
+    if ((err = launch_scored_logits(a, num_ctas, s)) != cudaSuccess) return err;
     int top = (a.T + kTopWarps - 1) / kTopWarps;
-    if (top > 6 * 148) top = 6 * 148;
+    if (top > 6 * num_ctas) top = 6 * num_ctas;
     if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
         return err;
     return launch_pdl(scored_scatter_kernel, dim3(nchunks), dim3(256), 0, s, a, (const int32_t*)sums);

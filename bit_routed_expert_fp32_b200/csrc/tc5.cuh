@@ -96,12 +96,13 @@ __device__ inline void umma_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Arrives on the barrier at this shared-memory offset in both CTAs of the pair.
-__device__ inline void umma_commit_pair(uint64_t* bar) {
+// Arrives on the barrier at this shared-memory offset in both CTAs of the pair (ctas: their
+// bits among the cluster's ranks).
+__device__ inline void umma_commit_pair(uint64_t* bar, uint16_t ctas = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(ctas)
         : "memory");
 }
 // A box into this CTA's shared memory whose bytes count on a barrier of either CTA of the
@@ -156,6 +157,66 @@ __device__ inline float4 ld_peer_v4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+// ---- waits ---------------------------------------------------------------------------------
+__device__ inline int ld_volatile(const int& v) { return *reinterpret_cast<const volatile int*>(&v); }
+__device__ inline void st_volatile(int& v, int x) { *reinterpret_cast<volatile int*>(&v) = x; }
+
+// Bounded wait of one CTA's thread: when it runs out, or another thread's has, the flag is up
+// and false is returned.
+__device__ inline bool wait_or_flag(int& abort_flag, uint64_t* bar, uint32_t parity, Ctrl* ctrl, uint32_t detail) {
+    if (ld_volatile(abort_flag)) return false;
+    if (mbar_wait_bounded(bar, parity, kWaitLimit)) return true;
+    st_volatile(abort_flag, 1);
+    report_error(ctrl, MOE_ERR_TIMEOUT, detail);
+    return false;
+}
+// The same for a thread of a CTA pair, which gives up at once when either CTA has.
+__device__ inline void pair_abort(int& abort_flag) {
+    st_volatile(abort_flag, 1);
+    st_peer_u32(map_peer(smem_u32(&abort_flag), cluster_rank() ^ 1), 1);
+}
+__device__ inline bool pair_wait(int& abort_flag, uint64_t* bar, uint32_t parity, Ctrl* ctrl, uint32_t detail) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!ld_volatile(abort_flag)) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > kWaitLimit) {
+            pair_abort(abort_flag);
+            report_error(ctrl, MOE_ERR_TIMEOUT, detail);
+        }
+    }
+    return false;
+}
+// Before a pair's producer leaves after an abort (one thread of each CTA): no copy may still
+// target shared memory.  The leader, on whose barriers the bytes of both CTAs count, waits
+// (bounded) for the last phase issued on every slot; the other CTA, which may have issued past
+// the leader, gives its last copies (microseconds) some half a millisecond.
+__device__ inline void pair_drain(uint64_t* full, int stages, int issued, bool leader, Ctrl* ctrl, uint32_t detail) {
+    if (leader) {
+        for (int d = 0; d < stages && d < issued; ++d) {
+            const int i = issued - 1 - d;
+            if (!mbar_wait_bounded(&full[i % stages], (uint32_t)(i / stages) & 1, kWaitLimit)) {
+                report_error(ctrl, MOE_ERR_TIMEOUT, detail);
+                return;
+            }
+        }
+    } else {
+        const long long c0 = clock64();
+        while (clock64() - c0 < 1000000) __nanosleep(1000);
+    }
+}
+// Failure-path tests (moe_workspace_set_test_stall): a warp's bounded wait on a barrier that
+// nothing completes; true when it ran out.
+__device__ inline bool test_stall(uint64_t* bar, uint32_t cycles, int lane) {
+    bool got = true;
+    if (lane == 0) got = mbar_wait_bounded(bar, 0, cycles);
+    got = __shfl_sync(0xffffffffu, got, 0);
+    __syncwarp();
+    return !got;
 }
 
 // Shared memory a CTA with `cols` tensor-memory columns must take at least: its share of the

@@ -153,7 +153,7 @@ def random_case(T, Hd, E, seed, bias, balance, k, **kw):
     raise RuntimeError("could not remove near-ties")
 
 
-@pytest.mark.parametrize("T", [1, 3, 8, 16, 31, 64, 65, 129, 700])
+@pytest.mark.parametrize("T", [1, 3, 8, 16, 31, 64, 65, 129, 257, 700, 2500, 5000])
 @pytest.mark.parametrize("Hd,E,k,G,tg,gt,sigmoid", [(64, 8, 2, 4, 2, 1, True), (192, 60, 8, 6, 3, 2, False),
                                                     (1024, 256, 8, 8, 4, 2, True), (7168, 256, 8, 8, 4, 2, True),
                                                     (2240, 130, 5, 1, 1, 1, False), (8256, 24, 4, 3, 2, 1, False)])
@@ -274,3 +274,25 @@ def test_repeats_bit_for_bit():
         a, c = (route(x[:n], wr, b, bal, 8, sigmoid=True) for _ in range(2))
         for name in a:
             np.testing.assert_array_equal(a[name], c[name])
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    import torch
+    import bit_routed_expert_fp32_b200 as moe
+    T, kw = 150, dict(sigmoid=True)
+    x, wr, _, _, L = random_case(T, 640, 64, 3, False, False, 4, **kw)
+    cfg = _cfg(640, 64, 4)
+    ws = torch.empty(moe.moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+    moe.moe_workspace_init(ws)
+    rt = moe.alloc_routing(cfg, T)
+    router = moe.Router(score=moe.SCORE_SIGMOID)
+    xd, wd = moe.bf16_to_device(x), torch.from_numpy(wr).cuda()
+    moe.moe_workspace_set_test_stall(ws, 1000)
+    moe.moe_route_scored(cfg, router, T, xd, wd, None, None, rt, ws)
+    st, det = moe.moe_get_error(ws)
+    assert moe.STATUS[st] == "MOE_ERR_TIMEOUT" and det & 0xF00 == moe.DETAIL["TEST_STALL"], (st, hex(det))
+    moe.moe_workspace_set_test_stall(ws, 0)
+    moe.moe_route_scored(cfg, router, T, xd, wd, None, None, rt, ws)
+    torch.cuda.synchronize()
+    assert moe.moe_get_error(ws) == (0, 0)
+    check({n: t.cpu().numpy() for n, t in rt.items()}, L, None, 4, 64, 2.0 ** -18, **kw)
