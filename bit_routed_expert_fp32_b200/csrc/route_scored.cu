@@ -145,9 +145,11 @@ __device__ inline uint32_t key32(float f) {
 }
 __device__ inline float unkey32(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
 
-// The choice in fp32 where fp32 decides it.  Scores from the fast exponential are off by less
-// than 1e-6 (its documented error of 2 + 1.17 |x| ulp counts in proportion to s (1 - s), or
-// to p); adding the balance rounds once more.  So where neighbours among the k + 1 largest
+// The choice in fp32 where fp32 decides it.  Sigmoid scores from the fast exponential (its
+// documented error of 2 + 1.17 |x| ulp counts in proportion to s (1 - s): 8e-8 at most), one
+// rounding and the fast quotient (two ulp) are off by at most 2.7e-7; softmax scores by at
+// most 2.6e-6 of the largest (ten ulp of the sum's terms on average, its thirteen additions,
+// the terms' own few ulp).  Adding the balance rounds once more.  So where neighbours among the k + 1 largest
 // values (and the group scores beside the border) lie further apart than both can be off,
 // their order is the exact one; otherwise, and where NaN or infinities meet, false is
 // returned and the careful path decides.  A softmax without balance has the order of its
@@ -155,7 +157,10 @@ __device__ inline float unkey32(uint32_t k) { return __uint_as_float((k & 0x8000
 // expert's place in the lane; a lane's eight are sorted once and then only popped.
 __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, const float (&L)[8], const float (&b)[8],
                                             Scratch& scratch, int lane, int& my_id) {
-    constexpr float kAbs = 4e-6f, kRel = 1.2e-6f;         // kRel: the rounding, and eight steps of a key
+    // what two scores can be off together, and, relative to their sum of sizes, what the
+    // rounding and eight steps of a key come to (2^-20 of either)
+    constexpr float kRel = 6e-7f;
+    float abs_err = 6e-7f;
     const bool grouped = r.top_groups < r.n_groups, by_logit = !r.sigmoid && !r.balance;
     float c[8], m = 0.f;
     if (r.sigmoid) {
@@ -174,7 +179,8 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
                 z += c[j];
             }
             z = warp_sum(z);
-            const float iz = __fdividef(1.f, z);
+            const float iz = __fdividef(1.f, z);          // also the largest score
+            abs_err = 6e-6f * iz;
 #pragma unroll
             for (int j = 0; j < 8; ++j) c[j] = c[j] * iz + b[j];
         }
@@ -237,7 +243,7 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
         const unsigned lanes = __ballot_sync(0xffffffffu, keep);
         const float lo = unkey32(__reduce_min_sync(0xffffffffu, keep && sc == sc ? key32(sc) : 0xFF800000u));
         const float hi = unkey32(__reduce_max_sync(0xffffffffu, in && !keep ? key32(sc) : 0x007FFFFFu));
-        if (__any_sync(0xffffffffu, in && sc != sc) || !(lo - hi > 2.f * kAbs + 2.f * kRel * (fabsf(lo) + fabsf(hi))))
+        if (__any_sync(0xffffffffu, in && sc != sc) || !(lo - hi > 2.f * abs_err + kRel * (fabsf(lo) + fabsf(hi))))
             return false;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -273,7 +279,7 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
     bool ok = true;
     if (lane < k) {
         const float w = unkey32(next & ~7u);
-        ok = next == 0 || v - w > (by_logit ? 0.f : kAbs) + kRel * (fabsf(v) + fabsf(w));
+        ok = next == 0 || v - w > (by_logit ? 0.f : abs_err) + kRel * (fabsf(v) + fabsf(w));
         if (by_logit) ok &= v - m > -700.f;
     }
     return __all_sync(0xffffffffu, ok);
@@ -539,25 +545,24 @@ __global__ void __launch_bounds__(256) scored_split_kernel(RouteArgs p, uint16_t
 // Top-k: a warp per token.  Adds to the histograms of the token's chunk (p.hist) and of its
 // span of kSpan chunks (integer atomics: the sums do not depend on their order), from which
 // the scatter kernel's CTAs form their bases by themselves.
-constexpr int kTopWarps = 8, kSpan = 16;
+constexpr int kTopWarps = 4, kSpan = 16;
 
-__global__ void __launch_bounds__(32 * kTopWarps, 3) scored_topk_kernel(RouteArgs p, ScoreArgs r, int32_t* sums) {
+__global__ void __launch_bounds__(32 * kTopWarps, 6) scored_topk_kernel(RouteArgs p, ScoreArgs r, int32_t* sums) {
     __shared__ Scratch s_scratch[kTopWarps];
     griddep_launch_dependents();
     griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kTopWarps + warp, c = t / kChunk;
+    if (t >= p.T) return;
     float bal[8];
     load_balance(r, p.E, lane, bal);
-    for (int t = blockIdx.x * kTopWarps + warp; t < p.T; t += gridDim.x * kTopWarps) {
-        const int c = t / kChunk;
-        int32_t* ids = p.r.topk_ids + (size_t)t * p.k;
-        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, s_scratch[warp], lane, ids,
-                      p.r.topk_w + (size_t)t * p.k, nullptr);
-        if (lane < p.k) {
-            const int e = ids[lane];                           // the lane's own write
-            atomicAdd(p.hist + (size_t)c * p.E + e, 1);
-            atomicAdd(sums + (size_t)(c / kSpan) * p.E + e, 1);
-        }
+    int32_t* ids = p.r.topk_ids + (size_t)t * p.k;
+    select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, s_scratch[warp], lane, ids, p.r.topk_w + (size_t)t * p.k,
+                  nullptr);
+    if (lane < p.k) {
+        const int e = ids[lane];                               // the lane's own write
+        atomicAdd(p.hist + (size_t)c * p.E + e, 1);
+        atomicAdd(sums + (size_t)(c / kSpan) * p.E + e, 1);
     }
 }
 
@@ -655,8 +660,7 @@ cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_
     cudaError_t err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
     if (err != cudaSuccess) return err;
     if ((err = launch_scored_logits(a, num_ctas, s)) != cudaSuccess) return err;
-    int top = (a.T + kTopWarps - 1) / kTopWarps;
-    if (top > 6 * num_ctas) top = 6 * num_ctas;
+    const int top = (a.T + kTopWarps - 1) / kTopWarps;
     if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
         return err;
     return launch_pdl(scored_scatter_kernel, dim3(nchunks), dim3(256), 0, s, a, (const int32_t*)sums);

@@ -7,9 +7,11 @@
 // half of the experts' rows; the planes are then read once per 256 tokens, which L2 can
 // deliver); a stage holds 64 of K: the tokens' box and three plane boxes.  The tensor core's
 // running sums are not rounded to nearest, so a chain through all of K would carry a bias
-// that grows with it: every stage's twelve MMAs (the small planes first) start a fresh
+// that grows with it: every second stage (the small planes first) starts a fresh
 // accumulator, two of them in turn, and eight warps add each to fp32 sums in registers while
-// the next is formed.  K is also cut over the pairs of a cluster when there are few tokens;
+// the next is formed (16384 tokens of the full-size layer, whole call: 193 us with an
+// accumulator per stage, which the adding warps then bound, 161 us with one per two, 158 us
+// with one per four).  K is also cut over the pairs of a cluster when there are few tokens;
 // the parts are added through shared memory in part order, in double-float with the bias, and
 // rounded once.
 #include "route_common.cuh"
@@ -20,6 +22,7 @@ namespace {
 
 using namespace tc5;
 
+constexpr int kDrain = 2;                  // stages per accumulator
 constexpr int kThreads = 384, kTok = 256, kStages = 3, kEpiWarps = 8;
 
 struct LogitArgs {
@@ -126,8 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int slot = 0;
         uint32_t par = 0;
         for (int i = 0; i < n_stage && ok; ++i) {
-            const int buf = i & 1;
-            ok = pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((i >> 1) & 1) ^ 1, p.ctrl, kDetWaitEmpty | 0x71) &&
+            const int g = i / kDrain, buf = g & 1;
+            const bool first = i % kDrain == 0, last = i % kDrain == kDrain - 1 || i == n_stage - 1;
+            ok = (!first || pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
+                                      kDetWaitEmpty | 0x71)) &&
                  pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x70);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
@@ -138,9 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k16 = 0; k16 < kBK / 16; ++k16)
                         umma_ss_pair(tmem + buf * p.en, ad0 + off + 2 * k16, bd0 + off + pl * (wbytes >> 4) + 2 * k16,
-                                     idesc, pl == 2 && k16 == 0 ? 0u : 1u);
+                                     idesc, first && pl == 2 && k16 == 0 ? 0u : 1u);
                 umma_commit_pair(&S.empty_[slot], pair_mask);
-                umma_commit_pair(&S.acc_full[buf], pair_mask);
+                if (last) umma_commit_pair(&S.acc_full[buf], pair_mask);
             }
             __syncwarp();
             if (++slot == kStages) {
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, half = (warp - 4) >> 2, cols = p.en / 2;
 #pragma unroll
         for (int c = 0; c < 128; ++c) acc[c] = 0.f;
-        for (int i = 0; i < n_stage; ++i) {
+        for (int i = 0; i < (n_stage + kDrain - 1) / kDrain; ++i) {
             const int buf = i & 1;
             if (!__all_sync(0xffffffffu, pair_wait(S.abort_flag, &S.acc_full[buf], (uint32_t)(i >> 1) & 1, p.ctrl,
                                                    kDetWaitFull | 0x71)))
