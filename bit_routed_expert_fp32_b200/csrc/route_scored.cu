@@ -25,117 +25,150 @@ __device__ inline unsigned long long score_key(double c) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(c + 0.0);
     return (b >> 63) ? ~b : (b | (1ull << 63));
 }
+__device__ inline double unkey(unsigned long long k) {
+    return __longlong_as_double((long long)((k >> 63) ? (k & ~(1ull << 63)) : ~k));
+}
 
-// Scratch of a warp that chooses: its token's logits (and the fast path's values for groups
-// that do not align with lanes), or the careful path's values.
-union Scratch {
-    struct {
-        float L[256], c[256];
-    } f;
-    double d[256];
+// e^x in fp64 for |x| <= 708, to about one ulp and without branches, so that a lane's eight
+// interleave: x = n ln 2 + r with ln 2 in two parts (the first of 42 bits: n times it is
+// exact; Cody and Waite's reduction), Taylor's series of e^r to r^13 (|r| <= ln 2 / 2: the
+// rest is below 2^-57), and n added to the exponent.
+__device__ __forceinline__ double exp_d(double x) {
+    constexpr double kRound = 6755399441055744.0;          // 1.5 * 2^52: adding it rounds to an integer
+    const double t = fma(x, 1.4426950408889634, kRound), n = t - kRound;
+    double r = fma(n, -0x1.62e42fefa38p-1, x);
+    r = fma(n, -0x1.ef35793c76730p-45, r);
+    double e = 1.0 / 6227020800.0;
+    e = fma(e, r, 1.0 / 479001600.0);
+    e = fma(e, r, 1.0 / 39916800.0);
+    e = fma(e, r, 1.0 / 3628800.0);
+    e = fma(e, r, 1.0 / 362880.0);
+    e = fma(e, r, 1.0 / 40320.0);
+    e = fma(e, r, 1.0 / 5040.0);
+    e = fma(e, r, 1.0 / 720.0);
+    e = fma(e, r, 1.0 / 120.0);
+    e = fma(e, r, 1.0 / 24.0);
+    e = fma(e, r, 1.0 / 6.0);
+    e = fma(e, r, 0.5);
+    e = fma(e, r, 1.0);
+    e = fma(e, r, 1.0);
+    return __hiloint2double(__double2hiint(e) + (__double2loint(t) << 20), __double2loint(e));
+}
+// 1 / y for normal y > 0 whose reciprocal is normal, to an ulp: the hardware's approximation
+// (about 20 bits) and two steps of Newton's iteration.
+__device__ __forceinline__ double recip_d(double y) {
+    double r;
+    asm("rcp.approx.ftz.f64 %0, %1;" : "=d"(r) : "d"(y));
+    r = fma(fma(-y, r, 1.0), r, r);
+    return fma(fma(-y, r, 1.0), r, r);
+}
+// The scores in fp64: sigmoid(l) (zero below -708, as the reciprocal of an overflowing sum),
+// and e^(l - m) of a softmax (zero below -708).
+__device__ __forceinline__ double sigmoid_d(float l) {
+    const double e = exp_d(fmin(fmax(-(double)l, -708.0), 708.0));
+    return l < -708.f ? 0.0 : l == l ? recip_d(1.0 + e) : (double)l;
+}
+__device__ __forceinline__ double softmax_term_d(float l, float m) {
+    const double d = (double)l - (double)m;
+    return d < -708.0 ? 0.0 : d == d ? exp_d(fmin(d, 708.0)) : d;
+}
+
+// Scratch of a warp that chooses: its token's logits, and the values by which it chooses (as
+// fp32 where groups do not align with lanes, as keys on the careful path).
+struct Scratch {
+    float L[256];
+    union {
+        float c[256];
+        unsigned long long key[256];
+    };
 };
 
-// One token's choice by one warp, in fp64 throughout: lane l holds experts 8l .. 8l+7 (L, -inf
-// past the last).  Each round takes the largest key over the warp in two 32-bit reductions
-// (high words, then the low words of those that tie), the lowest lane and the lowest expert
-// inside it first.  Leaves id and score of slot n in lane n < k.
-__device__ __noinline__ void choose_careful(const ScoreArgs& r, int E, int k, const float (&L)[8], Scratch& scratch,
-                                            int lane, int& my_id, double& my_s) {
-    double s[8];
-    if (r.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = 1.0 / (1.0 + exp(-(double)L[j]));
-    } else {
-        float m = L[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) m = fmaxf(m, L[j]);
-#pragma unroll
+// One token's choice by one warp, in fp64 throughout, for the few tokens that fp32 does not
+// decide.  Each round takes the largest key over the warp in two 32-bit reductions (high words,
+// then the low words of those that tie), the lowest expert among equals.  Returns the expert of
+// slot n in lane n < k.  The loops stay rolled: a token that comes here pays mostly for
+// fetching the instructions (unrolled, 13 us of a 20 us kernel at 8192 tokens).
+__device__ __noinline__ int choose_careful(const ScoreArgs& r, int E, int k, Scratch& S, int lane) {
+    float m = 0.f;
+    double iz = 1.0;
+    __syncwarp();
+    if (!r.sigmoid) {
+        m = -INFINITY;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32) m = fmaxf(m, S.L[e]);
+#pragma unroll 1
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         double z = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            s[j] = exp((double)L[j] - (double)m);
-            z += s[j];
-        }
-#pragma unroll
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32) z += softmax_term_d(S.L[e], m);
+#pragma unroll 1
         for (int o = 16; o; o >>= 1) z += shfl_xor_d(z, o);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] /= z;
+        iz = recip_d(z);
     }
-    unsigned long long key[8];
-    const bool grouped = r.top_groups < r.n_groups;
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = 8 * lane + j;
-        key[j] = 0;
+#pragma unroll 1
+    for (int e = lane; e < 256; e += 32) {
+        unsigned long long key = 0;
         if (e < E) {
-            const double c = r.balance ? s[j] + (double)__ldg(r.balance + e) : s[j];
-            key[j] = score_key(c);
-            if (grouped) scratch.d[e] = c == c ? c : -INFINITY;
+            double c = r.sigmoid ? sigmoid_d(S.L[e]) : softmax_term_d(S.L[e], m) * iz;
+            if (r.balance) c += (double)__ldg(r.balance + e);
+            key = score_key(c);
         }
+        S.key[e] = key;
     }
-    if (grouped) {
+    __syncwarp();
+    if (r.top_groups < r.n_groups) {
         const int gs = E / r.n_groups;
-        __syncwarp();
+        // lane g: the group's two largest; the lanes start at different experts of their
+        // groups (bank conflicts)
         double sc = -INFINITY;
         if (lane < r.n_groups) {
-            // the lanes start at different experts of their groups (bank conflicts)
-            double t1 = -INFINITY, t2 = -INFINITY;
+            unsigned long long t1 = 0, t2 = 0;
             int i = lane % gs;
+#pragma unroll 2
             for (int n = 0; n < gs; ++n) {
-                const double c = scratch.d[lane * gs + i];
-                if (c > t1) {
-                    t2 = t1;
-                    t1 = c;
-                } else if (c > t2) {
-                    t2 = c;
-                }
+                const unsigned long long c = S.key[lane * gs + i];
+                t2 = max(t2, min(t1, c));
+                t1 = max(t1, c);
                 if (++i == gs) i = 0;
             }
-            sc = r.group_top == 2 ? t1 + t2 : t1;
+            sc = r.group_top == 2 ? unkey(t1) + unkey(t2) : unkey(t1);
             if (sc != sc) sc = -INFINITY;
         }
         __syncwarp();
         int rank = 0;
+#pragma unroll 1
         for (int g = 0; g < r.n_groups; ++g) {
             const double o = __shfl_sync(0xffffffffu, sc, g);
             rank += o > sc || (o == sc && g < lane);
         }
         const unsigned kept = __ballot_sync(0xffffffffu, lane < r.n_groups && rank < r.top_groups);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (8 * lane + j < E && !((kept >> ((8 * lane + j) / gs)) & 1u)) key[j] = 0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 32)
+            if (!((kept >> (e / gs)) & 1u)) S.key[e] = 0;
+        __syncwarp();
     }
+    int my_id = 0;
+#pragma unroll 1
     for (int n = 0; n < k; ++n) {
-        unsigned long long bk = key[0];
-        int bj = 0;
-#pragma unroll
-        for (int j = 1; j < 8; ++j)
-            if (key[j] > bk) {              // strict: an equal key keeps the lower expert
-                bk = key[j];
-                bj = j;
+        unsigned long long bk = 0;
+        int be = lane;
+#pragma unroll 2
+        for (int e = lane; e < 256; e += 32) {
+            const unsigned long long c = S.key[e];
+            if (c > bk) {                   // strict: an equal key keeps the lower expert
+                bk = c;
+                be = e;
             }
+        }
         const uint32_t hi = (uint32_t)(bk >> 32), lo = (uint32_t)bk;
         const uint32_t mh = __reduce_max_sync(0xffffffffu, hi);
         const uint32_t ml = __reduce_max_sync(0xffffffffu, hi == mh ? lo : 0u);
-        const int wl = __ffs(__ballot_sync(0xffffffffu, hi == mh && lo == ml)) - 1;
-        const int wj = __shfl_sync(0xffffffffu, bj, wl);
-        double v = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j == wj) v = s[j];
-        v = __shfl_sync(0xffffffffu, v, wl);
-        if (lane == n) {
-            my_s = v;
-            my_id = 8 * wl + wj;
-        }
-        if (lane == wl) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j == wj) key[j] = 0;
-        }
+        const int e = (int)__reduce_min_sync(0xffffffffu, hi == mh && lo == ml ? (uint32_t)be : 0xFFFFu);
+        if (lane == n) my_id = e;
+        if (lane == (e & 31)) S.key[e] = 0;
+        __syncwarp();
     }
+    return my_id;
 }
 
 // Order-preserving 32-bit key of a value that is not NaN (0 is below every key) and back.
@@ -218,13 +251,13 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
         } else {
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) scratch.f.c[8 * lane + j] = c[j];
+            for (int j = 0; j < 8; ++j) scratch.c[8 * lane + j] = c[j];
             __syncwarp();
             t1 = t2 = -INFINITY;
             if (lane < r.n_groups) {
                 int i = lane % gs;
                 for (int n = 0; n < gs; ++n) {
-                    const float v = scratch.f.c[lane * gs + i];
+                    const float v = scratch.c[lane * gs + i];
                     t2 = fmaxf(t2, fminf(t1, v));
                     t1 = fmaxf(t1, v);
                     if (++i == gs) i = 0;
@@ -298,43 +331,40 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
 #pragma unroll
         for (int j = 0; j < 8; ++j) L[j] = 8 * lane + j < E ? ldcg_f32(row + 8 * lane + j) : -INFINITY;
     }
-    int my_id = 0;
-    double s = 0.0;
     __syncwarp();
-    if (choose_fast(r, E, k, L, b, scratch, lane, my_id)) {
-        // the chosen scores in fp64, one a lane; softmax scores relative to the largest logit,
-        // over the sum of all only where they are not renormalised
-        __syncwarp();
-        *reinterpret_cast<float4*>(scratch.f.L + 8 * lane) = make_float4(L[0], L[1], L[2], L[3]);
-        *reinterpret_cast<float4*>(scratch.f.L + 8 * lane + 4) = make_float4(L[4], L[5], L[6], L[7]);
-        __syncwarp();
-        const double l = lane < k ? (double)scratch.f.L[my_id] : 0.0;
-        if (r.sigmoid) {
-            s = 1.0 / (1.0 + exp(-l));
-        } else {
-            float m = L[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j) m = fmaxf(m, L[j]);
-            m = unkey32(__reduce_max_sync(0xffffffffu, key32(m)));
-            s = exp(l - (double)m);
-            if (!r.renormalise) {
-                double z = 0.0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z += exp((double)L[j] - (double)m);
-#pragma unroll
-                for (int o = 16; o; o >>= 1) z += shfl_xor_d(z, o);
-                s /= z;
-            }
-        }
+    *reinterpret_cast<float4*>(scratch.L + 8 * lane) = make_float4(L[0], L[1], L[2], L[3]);
+    *reinterpret_cast<float4*>(scratch.L + 8 * lane + 4) = make_float4(L[4], L[5], L[6], L[7]);
+    __syncwarp();
+    int my_id = 0;
+    if (!choose_fast(r, E, k, L, b, scratch, lane, my_id)) my_id = choose_careful(r, E, k, scratch, lane);
+    // the chosen scores in fp64, one a lane; softmax scores relative to the largest logit, over
+    // the sum of all only where they are not renormalised
+    const float l = lane < k ? scratch.L[my_id] : 0.f;
+    double s;
+    if (r.sigmoid) {
+        s = sigmoid_d(l);
     } else {
-        choose_careful(r, E, k, L, scratch, lane, my_id, s);
+        float m = L[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = fmaxf(m, L[j]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = softmax_term_d(l, m);
+        if (!r.renormalise) {
+            double z = 0.0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z += softmax_term_d(L[j], m);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) z += shfl_xor_d(z, o);
+            s *= recip_d(z);
+        }
     }
     double w = lane < k ? s : 0.0;
     if (r.renormalise) {
         double sum = w;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += shfl_xor_d(sum, o);
-        w = sum > 0.0 ? w / sum : 0.0;
+        w = sum > 0.0 ? w / sum : 0.0;                    // sums may be tiny: a full division
     }
     if (lane < k) {
         ids_out[lane] = my_id;
