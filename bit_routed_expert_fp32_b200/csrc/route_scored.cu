@@ -361,9 +361,9 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
     }
     double w = lane < k ? s : 0.0;
     if (r.renormalise) {
-        double sum = w;
+        double sum = w;                                   // of lanes 0 .. 15 (k <= 16)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += shfl_xor_d(sum, o);
+        for (int o = 8; o; o >>= 1) sum += shfl_xor_d(sum, o);
         w = sum > 0.0 ? w / sum : 0.0;                    // sums may be tiny: a full division
     }
     if (lane < k) {
@@ -381,42 +381,48 @@ __device__ inline void load_balance(const ScoreArgs& r, int E, int lane, float (
 
 // ---------------------------------------------------------------- up to kSmallT tokens
 // The router's fp32 rows are read once, straight into MMA fragments: a CTA takes 16 experts
-// and a part of K (the CTAs of a cluster share the experts), a warp every 64th 32-wide step.
-// A weight is split exactly into three bf16 pieces (each the rounding of what is left), so
+// and a part of K (the CTAs of a cluster share the experts), its warps 32-wide steps in turn.
+// A weight is split exactly into three bf16 pieces (each the upper bits of what is left), so
 // that x w1 + x w2 + x w3 on mma.sync has fp32-level products.  The order of K inside a
 // step is free as long as both operands follow it: lane (g, t) takes elements 8t .. 8t+7 of
 // its rows, 32 contiguous bytes, as the fragments of two MMAs.  A warp's sum is short (its
 // few steps, the small pieces in an accumulator of their own); warps and CTAs are added in
-// double-float.  The last CTA to finish (a ticket) chooses the experts and permutes.
-constexpr int kSmThreads = 256, kSmWarps = 8, kSmExperts = 16, kSmStep = 32;
+// double-float.  Up to 16 tokens the last CTA to finish (a ticket) chooses, a warp per token,
+// and permutes, while the others form the decode operands; above, the choice and the
+// permutation are the kernels that larger counts use, spread over the GPU.
+constexpr int kSmExperts = 16, kSmStep = 32, kSmParts = 8, kTailT = 16;
 
-template <int NTL>   // 8-token MMA columns
+template <int NTL, int NW>   // 8-token MMA columns, warps
 struct SmallSmem {
     union {
-        float part[kSmWarps][kSmExperts][8 * NTL];
-        Scratch scratch[kSmWarps];
+        float part[NW][kSmExperts][8 * NTL];
+        Scratch scratch[NW];
     };
     Df sum[kSmExperts][8 * NTL];
-    int32_t ids[kSmallT * 16];
+    int32_t ids[kTailT * 16];
+    float bal[256];
     int cnt[256];
     int off[257];
     int last;
 };
 
-__device__ inline uint32_t pack_bf16x2(float lo, float hi) {
-    return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
+// The leading bf16 pieces (the upper 16 bits) of two weights as a pair; the weights keep the
+// rest, exactly.  The 24 bits of a weight are used up by three of them.
+__device__ inline uint32_t next_plane(float& a, float& b) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    a -= __uint_as_float(ua & 0xFFFF0000u);
+    b -= __uint_as_float(ub & 0xFFFF0000u);
+    return __byte_perm(ua, ub, 0x7632);
 }
-__device__ inline float bf16_part(float w) { return __uint_as_float((uint32_t)f32_to_bf16_bits(w) << 16); }
 
-template <int NTL>
-__global__ void __launch_bounds__(kSmThreads) scored_small_kernel(RouteArgs p, ScoreArgs r, int parts) {
+template <int NTL, int NW>
+__global__ void __launch_bounds__(32 * NW, 2)
+    scored_small_kernel(RouteArgs p, ScoreArgs r, int parts, int32_t* sums) {
+    constexpr int kThreads = 32 * NW, U = NTL == 1 ? 4 : NTL <= 4 ? 2 : 1;
+    constexpr bool kTail = 8 * NTL <= kTailT;
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    SmallSmem<NTL>& S = *reinterpret_cast<SmallSmem<NTL>*>(smem_raw);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {          // no expert pass of this workspace runs now
-        p.ctrl->work[0] = 0;
-        p.ctrl->work[1] = 0;
-    }
-    griddep_launch_dependents();        // one wave of CTAs: the expert pass may start launching
+    SmallSmem<NTL, NW>& S = *reinterpret_cast<SmallSmem<NTL, NW>*>(smem_raw);
+    griddep_launch_dependents();        // one wave of CTAs: the next kernel may start launching
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int part = (int)cluster_rank(), e0 = (int)(blockIdx.x / parts) * kSmExperts;
     const int steps = p.H / kSmStep;
@@ -425,125 +431,156 @@ __global__ void __launch_bounds__(kSmThreads) scored_small_kernel(RouteArgs p, S
     for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) hi[n][c] = lo[n][c] = 0.f;
-    const bool r0 = e0 + g < p.E, r1 = e0 + g + 8 < p.E;
+    const bool rows[2] = {e0 + g < p.E, e0 + g + 8 < p.E};
     const float* w0 = p.Wr + (size_t)(e0 + g) * p.H + 8 * t4;
-    const float* w1 = w0 + (size_t)8 * p.H;
-#pragma unroll 2
-    for (int st = part * kSmWarps + warp; st < steps; st += parts * kSmWarps) {
-        const int k0 = st * kSmStep;
-        float w[2][8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4* src = reinterpret_cast<const float4*>((h ? w1 : w0) + k0);
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float4 a = (h ? r1 : r0) ? __ldg(src) : z, b = (h ? r1 : r0) ? __ldg(src + 1) : z;
-            w[h][0] = a.x; w[h][1] = a.y; w[h][2] = a.z; w[h][3] = a.w;
-            w[h][4] = b.x; w[h][5] = b.y; w[h][6] = b.z; w[h][7] = b.w;
+    griddep_wait();
+    if (blockIdx.x == 0) {
+        if (threadIdx.x == 0) {                             // no expert pass of this workspace runs now
+            p.ctrl->work[0] = 0;
+            p.ctrl->work[1] = 0;
         }
-        uint4 xv[NTL];
+        if (!kTail)                                        // the choice adds to them
+            for (int i = threadIdx.x; i < p.E; i += kThreads) p.hist[i] = sums[i] = 0;
+    }
+    if (kTail)                                             // for the choice: a late first read of it would wait for HBM
+        for (int i = threadIdx.x; i < 256; i += kThreads) S.bal[i] = r.balance && i < p.E ? __ldg(r.balance + i) : 0.f;
+    // U steps at a time: up to 8 tokens all of a warp's loads are on their way at once on the
+    // usual sizes
+    for (int st = part * NW + warp; st < steps; st += U * parts * NW) {
+        float w[U][2][8];
+        uint4 xv[U][NTL];
 #pragma unroll
-        for (int n = 0; n < NTL; ++n) {
-            const int t = 8 * n + g;
-            xv[n] = t < p.T ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.H + k0 + 8 * t4))
-                            : make_uint4(0, 0, 0, 0);
-        }
+        for (int u = 0; u < U; ++u) {
+            const int su = st + u * parts * NW, k0 = su * kSmStep;
+            const bool in = su < steps;
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-            uint32_t a[2][4];               // [row half][pair]
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float u = bf16_part(w[h][2 * q]), v = bf16_part(w[h][2 * q + 1]);
-                    a[h][q] = pack_bf16x2(u, v);
-                    w[h][2 * q] -= u;
-                    w[h][2 * q + 1] -= v;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const float4* src = reinterpret_cast<const float4*>(w0 + (size_t)8 * h * p.H + k0);
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 a = in && rows[h] ? __ldg(src) : z, b = in && rows[h] ? __ldg(src + 1) : z;
+                w[u][h][0] = a.x; w[u][h][1] = a.y; w[u][h][2] = a.z; w[u][h][3] = a.w;
+                w[u][h][4] = b.x; w[u][h][5] = b.y; w[u][h][6] = b.z; w[u][h][7] = b.w;
+            }
 #pragma unroll
             for (int n = 0; n < NTL; ++n) {
-                float(&d)[4] = pl == 0 ? hi[n] : lo[n];
-                mma_bf16_16816(d[0], d[1], d[2], d[3], a[0][0], a[1][0], a[0][1], a[1][1], xv[n].x, xv[n].y);
-                mma_bf16_16816(d[0], d[1], d[2], d[3], a[0][2], a[1][2], a[0][3], a[1][3], xv[n].z, xv[n].w);
+                const int t = 8 * n + g;
+                xv[u][n] = in && t < p.T
+                               ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.H + k0 + 8 * t4))
+                               : make_uint4(0, 0, 0, 0);
             }
         }
-    }
-    // the decode operands of (token, group) pairs, one per warp
-    if (p.ops) {
-        const int G8 = 8 * ((p.H / 64 + 7) / 8);
-        const OperandArgs o{p.T, p.H, p.x, p.zx, p.iq, p.ctrl};
-        for (int pr = blockIdx.x * kSmWarps + warp; pr < p.T * G8; pr += gridDim.x * kSmWarps) {
-            compute_z(o, pr / G8, pr % G8, lane);
-            if (p.iq) compute_iq(o, pr / G8, pr % G8, lane);
-        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int pl = 0; pl < 3; ++pl) {
+                uint32_t a[2][4];               // [row half][pair]
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) a[h][q] = next_plane(w[u][h][2 * q], w[u][h][2 * q + 1]);
+#pragma unroll
+                for (int n = 0; n < NTL; ++n) {
+                    float(&d)[4] = pl == 0 ? hi[n] : lo[n];
+                    mma_bf16_16816(d[0], d[1], d[2], d[3], a[0][0], a[1][0], a[0][1], a[1][1], xv[u][n].x, xv[u][n].y);
+                    mma_bf16_16816(d[0], d[1], d[2], d[3], a[0][2], a[1][2], a[0][3], a[1][3], xv[u][n].z, xv[u][n].w);
+                }
+            }
     }
 #pragma unroll
     for (int n = 0; n < NTL; ++n)
 #pragma unroll
         for (int c = 0; c < 4; ++c) S.part[warp][g + 8 * (c >> 1)][8 * n + 2 * t4 + (c & 1)] = hi[n][c] + lo[n][c];
     __syncthreads();
-    for (int i = threadIdx.x; i < kSmExperts * 8 * NTL; i += kSmThreads) {
+    for (int i = threadIdx.x; i < kSmExperts * 8 * NTL; i += kThreads) {
         const int e = i / (8 * NTL), t = i % (8 * NTL);
         Df v = Df{S.part[0][e][t], 0.f};
 #pragma unroll
-        for (int u = 1; u < kSmWarps; ++u) v = df_add(v, Df{S.part[u][e][t], 0.f});
+        for (int u = 1; u < NW; ++u) v = df_add(v, Df{S.part[u][e][t], 0.f});
         S.sum[e][t] = v;
     }
     __syncthreads();
     cluster_sync();
-    for (int i = part * kSmThreads + threadIdx.x; i < kSmExperts * p.T; i += parts * kSmThreads) {
+    for (int i = part * kThreads + threadIdx.x; i < kSmExperts * p.T; i += parts * kThreads) {
         const int t = i / kSmExperts, e = i % kSmExperts;
         if (e0 + e >= p.E) continue;
         const uint32_t at = smem_u32(&S.sum[e][t]);
-        Df v = Df{0.f, 0.f};
-        for (int q = 0; q < parts; ++q) {
-            Df w;
-            asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
-                         : "=f"(w.hi), "=f"(w.lo)
-                         : "r"(map_peer(at, q))
-                         : "memory");
-            v = q ? df_add(v, w) : w;
-        }
-        // the bias and the one final rounding
-        p.logits[(size_t)t * p.E + e0 + e] =
-            (float)((double)v.hi + (double)v.lo + (p.bias ? (double)p.bias[e0 + e] : 0.0));
+        Df w[kSmParts];
+#pragma unroll
+        for (int q = 0; q < kSmParts; ++q)
+            if (q < parts)
+                asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                             : "=f"(w[q].hi), "=f"(w[q].lo)
+                             : "r"(map_peer(at, q))
+                             : "memory");
+        Df v = w[0];
+#pragma unroll
+        for (int q = 1; q < kSmParts; ++q)
+            if (q < parts) v = df_add(v, w[q]);
+        if (p.bias) v = df_add(v, Df{__ldg(p.bias + e0 + e), 0.f});
+        p.logits[(size_t)t * p.E + e0 + e] = v.hi + v.lo;      // the one rounding
     }
-    __threadfence();
-    __syncthreads();
-    cluster_sync();                     // no CTA's sums go away while another reads them
-    if (threadIdx.x == 0) S.last = atomicAdd(&p.ctrl->route_ticket, 1u) == gridDim.x - 1;
-    __syncthreads();
-    if (!S.last) return;
-    __threadfence();
-
-    for (int i = threadIdx.x; i < 256; i += kSmThreads) S.cnt[i] = 0;
-    float bal[8];
-    load_balance(r, p.E, lane, bal);
-    for (int t = warp; t < p.T; t += kSmWarps)
-        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, S.scratch[warp], lane, p.r.topk_ids + (size_t)t * p.k,
-                      p.r.topk_w + (size_t)t * p.k, S.ids + t * p.k);
-    __syncthreads();
-    for (int i = threadIdx.x; i < p.T * p.k; i += kSmThreads) atomicAdd(&S.cnt[S.ids[i]], 1);
-    __syncthreads();
-    if (warp == 0) {
-        warp_scan_counts(S.cnt, S.off, p.E, lane);
-        __syncwarp();
-        for (int i = lane; i < p.E; i += 32) {
-            p.r.counts[i] = S.cnt[i];
-            p.r.offsets[i] = S.off[i];
-        }
-        if (lane == 0) p.r.offsets[p.E] = S.off[p.E];
-        __syncwarp();
-        // off doubles as the running position per expert
-        warp_scatter(S.ids, 0, p.T * p.k, S.off, p.r.perm, p.r.inv_perm, lane, p.E);
-        if (lane == 0) p.ctrl->route_ticket = 0;
-    } else if (warp == 1) {
-        warp_active(S.cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
+    __syncwarp();
+    cluster_arrive();                   // a CTA leaves only when its sums have been read
+    if (kTail) {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) S.last = atomicAdd(&p.ctrl->route_ticket, 1u) == gridDim.x - 1;
+        __syncthreads();
     }
+    const bool last = kTail && S.last;
+    if (last) {
+        __threadfence();
+        for (int i = threadIdx.x; i < 256; i += kThreads) S.cnt[i] = 0;
+        __syncthreads();
+        if (warp < p.T) {
+            float bal[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) bal[j] = S.bal[8 * lane + j];
+            for (int t = warp; t < p.T; t += NW) {
+                select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, S.scratch[warp], lane,
+                              p.r.topk_ids + (size_t)t * p.k, p.r.topk_w + (size_t)t * p.k, S.ids + t * p.k);
+                __syncwarp();
+                if (lane < p.k) atomicAdd(&S.cnt[S.ids[t * p.k + lane]], 1);
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            warp_scan_counts(S.cnt, S.off, p.E, lane);
+            __syncwarp();
+            for (int i = lane; i < p.E; i += 32) {
+                p.r.counts[i] = S.cnt[i];
+                p.r.offsets[i] = S.off[i];
+            }
+            if (lane == 0) p.r.offsets[p.E] = S.off[p.E];
+            __syncwarp();
+            // off doubles as the running position per expert
+            warp_scatter(S.ids, 0, p.T * p.k, S.off, p.r.perm, p.r.inv_perm, lane, p.E);
+            if (lane == 0) p.ctrl->route_ticket = 0;
+        } else if (warp == 1) {
+            warp_active(S.cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
+        }
+    }
+    // the decode operands of (token, group) pairs, one per warp
+    if (p.ops && !(last && warp < 2)) {
+        const int G8 = 8 * ((p.H / 64 + 7) / 8);
+        const OperandArgs o{p.T, p.H, p.x, p.zx, p.iq, p.ctrl};
+        // the last CTA's share falls to its warps past the permutation's two
+        const int w = last ? warp - 2 : warp, nw = last ? NW - 2 : NW;
+        for (int base = blockIdx.x * NW; base < p.T * G8; base += gridDim.x * NW)
+            for (int v = w; v < NW; v += nw) {
+                const int pr = base + v;
+                if (pr >= p.T * G8) break;
+                compute_z(o, pr / G8, pr % G8, lane);
+                if (p.iq) compute_iq(o, pr / G8, pr % G8, lane);
+            }
+    }
+    __syncwarp();
+    cluster_wait();
 }
 
 // ---------------------------------------------------------------- above kSmallT tokens
 // The router's rows as three bf16 planes [3][E][H] (w = w1 + w2 + w3 exactly, each the
-// rounding of what is left), for the logits kernel's operand loads; zeroes the histograms
+// upper bits of what is left), for the logits kernel's operand loads; zeroes the histograms
 // that the top-k kernel adds to.
 __global__ void __launch_bounds__(256) scored_split_kernel(RouteArgs p, uint16_t* planes, int32_t* sums, int n_sums) {
     griddep_launch_dependents();
@@ -561,12 +598,7 @@ __global__ void __launch_bounds__(256) scored_split_kernel(RouteArgs p, uint16_t
         for (int pl = 0; pl < 3; ++pl) {
             uint32_t o[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float u = bf16_part(w[2 * q]), v = bf16_part(w[2 * q + 1]);
-                o[q] = pack_bf16x2(u, v);
-                w[2 * q] -= u;
-                w[2 * q + 1] -= v;
-            }
+            for (int q = 0; q < 4; ++q) o[q] = next_plane(w[2 * q], w[2 * q + 1]);
             *reinterpret_cast<uint4*>(planes + pl * plane + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
@@ -652,44 +684,49 @@ __global__ void __launch_bounds__(256) scored_scatter_kernel(RouteArgs p, const 
     if (warp == 1) warp_active(s_cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
 }
 
-template <int NTL>
-cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, cudaStream_t s) {
-    const size_t smem = sizeof(SmallSmem<NTL>);
-    const cudaError_t err = set_smem_limit(scored_small_kernel<NTL>, smem);
+template <int NTL, int NW>
+cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, int32_t* sums, cudaStream_t s) {
+    const size_t smem = sizeof(SmallSmem<NTL, NW>);
+    const cudaError_t err = set_smem_limit(scored_small_kernel<NTL, NW>, smem);
     if (err != cudaSuccess) return err;
     // K parts: up to eight CTAs of a cluster, each warp of them with at least one step
-    int parts = 8;
-    while (parts > 1 && parts * kSmWarps > a.H / kSmStep) parts /= 2;
+    int parts = kSmParts;
+    while (parts > 1 && parts * NW > a.H / kSmStep) parts /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.E + kSmExperts - 1) / kSmExperts * parts);
-    cfg.blockDim = dim3(kSmThreads);
+    cfg.blockDim = dim3(32 * NW);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = parts;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = parts;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, scored_small_kernel<NTL>, a, r, parts);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, scored_small_kernel<NTL, NW>, a, r, parts, sums);
 }
 
 }  // namespace
 
 cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_ctas, cudaStream_t s) {
-    if (a.T <= kSmallT) {
-        if (a.T <= 8) return launch_small<1>(a, r, s);
-        if (a.T <= 16) return launch_small<2>(a, r, s);
-        if (a.T <= 32) return launch_small<4>(a, r, s);
-        return launch_small<8>(a, r, s);
-    }
-    // the spans' sums and the planes take regions of the workspace that only moe_forward uses
     const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
-    int32_t* sums = reinterpret_cast<int32_t*>(a.zx);
-    cudaError_t err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
+    cudaError_t err;
+    int32_t* sums;
+    if (a.T <= kSmallT) {
+        sums = reinterpret_cast<int32_t*>(a.planes);       // the region moe_forward's sums take
+        if (a.T <= 8) return launch_small<1, 8>(a, r, sums, s);
+        if (a.T <= kTailT) return launch_small<2, 8>(a, r, sums, s);
+        err = a.T <= 32 ? launch_small<4, 8>(a, r, sums, s) : launch_small<8, 8>(a, r, sums, s);
+    } else {
+        // the spans' sums and the planes take regions of the workspace that only moe_forward uses
+        sums = reinterpret_cast<int32_t*>(a.zx);
+        err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
+        if (err == cudaSuccess) err = launch_scored_logits(a, num_ctas, s);
+    }
     if (err != cudaSuccess) return err;
-    if ((err = launch_scored_logits(a, num_ctas, s)) != cudaSuccess) return err;
     const int top = (a.T + kTopWarps - 1) / kTopWarps;
     if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
         return err;
