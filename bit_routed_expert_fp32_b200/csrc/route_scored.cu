@@ -364,7 +364,7 @@ __device__ void select_scored(const ScoreArgs& r, int E, int k, const float* row
         double sum = w;                                   // of lanes 0 .. 15 (k <= 16)
 #pragma unroll
         for (int o = 8; o; o >>= 1) sum += shfl_xor_d(sum, o);
-        w = sum > 0.0 ? w / sum : 0.0;                    // sums may be tiny: a full division
+        w = sum > 1e-280 ? w * recip_d(sum) : sum > 0.0 ? w / sum : 0.0;
     }
     if (lane < k) {
         ids_out[lane] = my_id;
@@ -387,10 +387,11 @@ __device__ inline void load_balance(const ScoreArgs& r, int E, int lane, float (
 // step is free as long as both operands follow it: lane (g, t) takes elements 8t .. 8t+7 of
 // its rows, 32 contiguous bytes, as the fragments of two MMAs.  A warp's sum is short (its
 // few steps, the small pieces in an accumulator of their own); warps and CTAs are added in
-// double-float.  Up to 16 tokens the last CTA to finish (a ticket) chooses, a warp per token,
-// and permutes, while the others form the decode operands; above, the choice and the
-// permutation are the kernels that larger counts use, spread over the GPU.
-constexpr int kSmExperts = 16, kSmStep = 32, kSmParts = 8, kTailT = 16;
+// double-float.  Up to 8 tokens the last CTA to finish (a ticket) chooses, a warp per token,
+// and permutes, while the others form the decode operands; above, one CTA of 32 warps does
+// that in a kernel of its own (16 tokens: 17.7 us with a last CTA of 16 warps, 17.3 us with
+// the two kernels of larger counts, CHOOSE_US with one).
+constexpr int kSmExperts = 16, kSmStep = 32, kSmParts = 8, kTailT = 8;
 
 template <int NTL, int NW>   // 8-token MMA columns, warps
 struct SmallSmem {
@@ -417,7 +418,7 @@ __device__ inline uint32_t next_plane(float& a, float& b) {
 
 template <int NTL, int NW>
 __global__ void __launch_bounds__(32 * NW, 2)
-    scored_small_kernel(RouteArgs p, ScoreArgs r, int parts, int32_t* sums) {
+    scored_small_kernel(RouteArgs p, ScoreArgs r, int parts) {
     constexpr int kThreads = 32 * NW, U = NTL == 1 ? 4 : NTL <= 4 ? 2 : 1;
     constexpr bool kTail = 8 * NTL <= kTailT;
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -434,13 +435,9 @@ __global__ void __launch_bounds__(32 * NW, 2)
     const bool rows[2] = {e0 + g < p.E, e0 + g + 8 < p.E};
     const float* w0 = p.Wr + (size_t)(e0 + g) * p.H + 8 * t4;
     griddep_wait();
-    if (blockIdx.x == 0) {
-        if (threadIdx.x == 0) {                             // no expert pass of this workspace runs now
-            p.ctrl->work[0] = 0;
-            p.ctrl->work[1] = 0;
-        }
-        if (!kTail)                                        // the choice adds to them
-            for (int i = threadIdx.x; i < p.E; i += kThreads) p.hist[i] = sums[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {              // no expert pass of this workspace runs now
+        p.ctrl->work[0] = 0;
+        p.ctrl->work[1] = 0;
     }
     if (kTail)                                             // for the choice: a late first read of it would wait for HBM
         for (int i = threadIdx.x; i < 256; i += kThreads) S.bal[i] = r.balance && i < p.E ? __ldg(r.balance + i) : 0.f;
@@ -561,7 +558,7 @@ __global__ void __launch_bounds__(32 * NW, 2)
         }
     }
     // the decode operands of (token, group) pairs, one per warp
-    if (p.ops && !(last && warp < 2)) {
+    if (kTail && p.ops && !(last && warp < 2)) {
         const int G8 = 8 * ((p.H / 64 + 7) / 8);
         const OperandArgs o{p.T, p.H, p.x, p.zx, p.iq, p.ctrl};
         // the last CTA's share falls to its warps past the permutation's two
@@ -576,6 +573,72 @@ __global__ void __launch_bounds__(32 * NW, 2)
     }
     __syncwarp();
     cluster_wait();
+}
+
+// The choice and the permutation of up to kSmallT tokens: one CTA, a warp per token at a time;
+// then eight warps rank a contiguous share of the pairs each.  The other CTAs form the decode
+// operands of (token, group) pairs meanwhile, one per warp.
+struct ChooseSmem {
+    union {
+        Scratch scratch[32];
+        int run[8][256];
+    };
+    int32_t ids[kSmallT * 16];
+    int cnt[256];
+    int off[257];
+};
+
+__global__ void __launch_bounds__(1024) scored_choose_kernel(RouteArgs p, ScoreArgs r) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    ChooseSmem& S = *reinterpret_cast<ChooseSmem*>(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.k;
+    if (threadIdx.x < 256) S.cnt[threadIdx.x] = 0;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (blockIdx.x > 0) {
+        const int G8 = 8 * ((p.H / 64 + 7) / 8), pr = (int)(blockIdx.x - 1) * 32 + warp;
+        if (pr < p.T * G8) {
+            const OperandArgs o{p.T, p.H, p.x, p.zx, p.iq, p.ctrl};
+            compute_z(o, pr / G8, pr % G8, lane);
+            if (p.iq) compute_iq(o, pr / G8, pr % G8, lane);
+        }
+        return;
+    }
+    float bal[8];
+    load_balance(r, p.E, lane, bal);
+    __syncthreads();
+    for (int t = warp; t < p.T; t += 32) {
+        select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, S.scratch[warp], lane, p.r.topk_ids + (size_t)t * p.k,
+                      p.r.topk_w + (size_t)t * p.k, S.ids + t * p.k);
+        __syncwarp();
+        if (lane < p.k) atomicAdd(&S.cnt[S.ids[t * p.k + lane]], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * 256; i += 1024) S.run[i >> 8][i & 255] = 0;
+    __syncthreads();
+    const int share = (n + 255) / 256 * 32, b0 = min(n, warp * share), b1 = min(n, b0 + share);
+    if (warp < 8)
+        for (int i = b0 + lane; i < b1; i += 32) atomicAdd(&S.run[warp][S.ids[i]], 1);
+    else if (warp == 8)
+        warp_scan_counts(S.cnt, S.off, p.E, lane);
+    else if (warp == 9)
+        warp_active(S.cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
+    __syncthreads();
+    const int e = threadIdx.x;
+    if (e < p.E) {
+        int run = S.off[e];
+        p.r.counts[e] = S.cnt[e];
+        p.r.offsets[e] = run;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const int v = S.run[w][e];
+            S.run[w][e] = run;
+            run += v;
+        }
+    }
+    if (e == 0) p.r.offsets[p.E] = S.off[p.E];
+    __syncthreads();
+    if (warp < 8) warp_scatter(S.ids + b0, b0, b1 - b0, S.run[warp], p.r.perm, p.r.inv_perm, lane, p.E);
 }
 
 // ---------------------------------------------------------------- above kSmallT tokens
@@ -685,7 +748,7 @@ __global__ void __launch_bounds__(256) scored_scatter_kernel(RouteArgs p, const 
 }
 
 template <int NTL, int NW>
-cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, int32_t* sums, cudaStream_t s) {
+cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, cudaStream_t s) {
     const size_t smem = sizeof(SmallSmem<NTL, NW>);
     const cudaError_t err = set_smem_limit(scored_small_kernel<NTL, NW>, smem);
     if (err != cudaSuccess) return err;
@@ -706,27 +769,27 @@ cudaError_t launch_small(const RouteArgs& a, const ScoreArgs& r, int32_t* sums, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, scored_small_kernel<NTL, NW>, a, r, parts, sums);
+    return cudaLaunchKernelEx(&cfg, scored_small_kernel<NTL, NW>, a, r, parts);
 }
 
 }  // namespace
 
 cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_ctas, cudaStream_t s) {
-    const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
     cudaError_t err;
-    int32_t* sums;
     if (a.T <= kSmallT) {
-        sums = reinterpret_cast<int32_t*>(a.planes);       // the region moe_forward's sums take
-        if (a.T <= 8) return launch_small<1, 8>(a, r, sums, s);
-        if (a.T <= kTailT) return launch_small<2, 8>(a, r, sums, s);
-        err = a.T <= 32 ? launch_small<4, 8>(a, r, sums, s) : launch_small<8, 8>(a, r, sums, s);
-    } else {
-        // the spans' sums and the planes take regions of the workspace that only moe_forward uses
-        sums = reinterpret_cast<int32_t*>(a.zx);
-        err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
-        if (err == cudaSuccess) err = launch_scored_logits(a, num_ctas, s);
+        if (a.T <= kTailT) return launch_small<1, 8>(a, r, s);
+        err = a.T <= 16 ? launch_small<2, 8>(a, r, s) : a.T <= 32 ? launch_small<4, 8>(a, r, s) : launch_small<8, 8>(a, r, s);
+        if (err == cudaSuccess) err = set_smem_limit(scored_choose_kernel, sizeof(ChooseSmem));
+        if (err != cudaSuccess) return err;
+        const int pairs = a.ops ? a.T * 8 * ((a.H / 64 + 7) / 8) : 0;
+        return launch_pdl(scored_choose_kernel, dim3(1 + (pairs + 31) / 32), dim3(1024), sizeof(ChooseSmem), s, a, r);
     }
+    // the spans' sums and the planes take regions of the workspace that only moe_forward uses
+    const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
+    int32_t* sums = reinterpret_cast<int32_t*>(a.zx);
+    err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
     if (err != cudaSuccess) return err;
+    if ((err = launch_scored_logits(a, num_ctas, s)) != cudaSuccess) return err;
     const int top = (a.T + kTopWarps - 1) / kTopWarps;
     if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
         return err;
