@@ -214,6 +214,10 @@ cudaError_t launch_combine_pairs(int T, int k, int H, int n_rows, const float* r
 // gate-weighted unpermute-combine of the partial rows into y
 cudaError_t launch_combine(const FfnArgs& a, cudaStream_t s);
 
+// Clusters of `size` CTAs (per_sm of which share an SM, 1 .. 3) that are resident at once on
+// the current device, num_ctas its SMs (capacity.cu)
+int cluster_capacity(int size, int per_sm, int num_ctas);
+
 // Dense matrix product with its epilogue (linear.cu); arguments as in moe_linear.
 struct LinearArgs {
     int T, N, K;

@@ -276,12 +276,13 @@ def test_repeats_bit_for_bit():
             np.testing.assert_array_equal(a[name], c[name])
 
 
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+@pytest.mark.parametrize("T,E", [(150, 64), (6000, 256)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T, E):
     import torch
     import bit_routed_expert_fp32_b200 as moe
-    T, kw = 150, dict(sigmoid=True)
-    x, wr, _, _, L = random_case(T, 640, 64, 3, False, False, 4, **kw)
-    cfg = _cfg(640, 64, 4)
+    kw = dict(sigmoid=True)
+    x, wr, _, _, L = random_case(T, 640, E, 3, False, False, 4, **kw)
+    cfg = _cfg(640, E, 4)
     ws = torch.empty(moe.moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
     moe.moe_workspace_init(ws)
     rt = moe.alloc_routing(cfg, T)
@@ -295,4 +296,4 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     moe.moe_route_scored(cfg, router, T, xd, wd, None, None, rt, ws)
     torch.cuda.synchronize()
     assert moe.moe_get_error(ws) == (0, 0)
-    check({n: t.cpu().numpy() for n, t in rt.items()}, L, None, 4, 64, 2.0 ** -18, **kw)
+    check({n: t.cpu().numpy() for n, t in rt.items()}, L, None, 4, E, 2.0 ** -18, **kw)
