@@ -722,9 +722,186 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t s) {
     return launch_pdl(linear_pair_kernel<F16, GLU>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, s, p, wm, xm);
 }
 
+// ---------------------------------------------------------------- a few tokens
+// One to kVecTok tokens: the weights' bytes are all that counts, and the tile kernel's fixed
+// steps (tensor memory, two cluster barriers) cost as much as reading them.  Here a warp takes
+// four weight rows (two outputs' gate and up rows with SwiGLU) and a part of K, 16 bytes a
+// lane and row at a time, in fp32 FMAs; K is cut over the warps of a CTA, whose sums meet in
+// shared memory in part order.
+constexpr int kVecWarps = 8, kVecRows = 4, kVecTok = 4;
+
+struct VecArgs {
+    int T, N, K, act, res_f32;
+    int parts;               // K parts: 1, 2, 4 or 8 warps of a CTA share their rows
+    int64_t ldx, ldw, ldr, ldy;
+    const uint16_t *x, *w, *bias;
+    const void* res;
+    uint16_t* y;
+};
+
+template <bool F16>
+__device__ inline void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (F16) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            f[2 * j] = p.x;
+            f[2 * j + 1] = p.y;
+        } else {
+            f[2 * j] = __uint_as_float(u[j] << 16);
+            f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+    }
+}
+// 16 bytes that are read once (they stay out of L1).
+__device__ inline uint4 ld_stream(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+// Eight elements at k of a row of K, zero past its end.
+__device__ inline uint4 load8(const uint16_t* row, int k, int K) {
+    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    uint32_t u[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (k + j < K) u[j >> 1] |= (uint32_t)row[k + j] << (16 * (j & 1));
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+template <bool F16, bool GLU, int NT>
+__global__ void __launch_bounds__(32 * kVecWarps) linear_vec_kernel(const __grid_constant__ VecArgs p) {
+    constexpr int kOut = GLU ? kVecRows / 2 : kVecRows;  // outputs of a warp
+    constexpr int U = NT == 1 ? 4 : NT == 2 ? 2 : 1;     // steps whose loads are issued together
+    __shared__ float s_sum[kVecWarps][kVecRows][NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = kVecWarps / p.parts, grp = warp / p.parts, part = warp - grp * p.parts;
+    const int n0 = (blockIdx.x * groups + grp) * kOut;
+    const int steps = (p.K + 255) / 256, s0 = part * steps / p.parts, s1 = (part + 1) * steps / p.parts;
+    griddep_launch_dependents();
+    const uint16_t* rows[kVecRows];
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) {
+        const int n = n0 + r % kOut;
+        rows[r] = p.w + (n < p.N ? n + (int64_t)(r / kOut) * p.N : 0) * p.ldw;
+    }
+    float acc[kVecRows][NT];
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
+    griddep_wait();
+    auto add = [&](const uint4(&wv)[kVecRows], const uint4(&xv)[NT]) {
+        float xf[NT][8];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) unpack8<F16>(xv[t], xf[t]);
+#pragma unroll
+        for (int r = 0; r < kVecRows; ++r) {
+            float wf[8];
+            unpack8<F16>(wv[r], wf);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[r][t] = fmaf(wf[j], xf[t][j], acc[r][t]);
+        }
+    };
+    // whole blocks of U steps without a condition (rows past the last output read row 0, tokens
+    // past the last the first token), so that their loads go out together; then the rest
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xr[t] = p.x + (t < p.T ? t : 0) * p.ldx;
+    int s = s0;
+    for (; s + U <= s1 && (s + U) * 256 <= p.K; s += U) {
+        uint4 wv[U][kVecRows], xv[U][NT];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int k = (s + u) * 256 + lane * 8;
+#pragma unroll
+            for (int r = 0; r < kVecRows; ++r) wv[u][r] = ld_stream(rows[r] + k);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xv[u][t] = __ldg(reinterpret_cast<const uint4*>(xr[t] + k));
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) add(wv[u], xv[u]);
+    }
+    for (; s < s1; ++s) {
+        const int k = s * 256 + lane * 8;
+        uint4 wv[kVecRows], xv[NT];
+#pragma unroll
+        for (int r = 0; r < kVecRows; ++r) wv[r] = k < p.K ? load8(rows[r], k, p.K) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) xv[t] = k < p.K ? load8(xr[t], k, p.K) : make_uint4(0, 0, 0, 0);
+        add(wv, xv);
+    }
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float v = acc[r][t];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+            if (lane == 0) s_sum[warp][r][t] = v;
+        }
+    __syncthreads();
+    // one output a thread
+    const int i = threadIdx.x;
+    if (i >= groups * kOut * p.T) return;
+    const int t = i / (groups * kOut), o = i - t * groups * kOut, g = o / kOut, r = o - g * kOut;
+    const int n = (blockIdx.x * groups + g) * kOut + r;
+    if (n >= p.N) return;
+    float a = 0.f, b = 0.f;
+    for (int q = 0; q < p.parts; ++q) {
+        a += s_sum[g * p.parts + q][r][t];
+        if (GLU) b += s_sum[g * p.parts + q][kOut + r][t];
+    }
+    if (p.bias) {
+        a += to_f32<F16>(__ldg(p.bias + n));
+        if (GLU) b += to_f32<F16>(__ldg(p.bias + p.N + n));
+    }
+    float v = GLU ? silu_fast(a) * b : apply_act(p.act, a);
+    if (p.res) {
+        const int64_t ri = t * p.ldr + n;
+        v += p.res_f32 ? static_cast<const float*>(p.res)[ri] : to_f32<F16>(static_cast<const uint16_t*>(p.res)[ri]);
+    }
+    p.y[t * p.ldy + n] = from_f32<F16>(v);
+}
+
+template <bool F16, bool GLU, int NT>
+cudaError_t launch_vec(const LinearArgs& a, cudaStream_t s) {
+    constexpr int kOut = GLU ? kVecRows / 2 : kVecRows;
+    VecArgs p = {a.T, a.N, a.K, a.act, a.res_f32, 1, a.ldx, a.ldw, a.ldr, a.ldy, static_cast<const uint16_t*>(a.x),
+                 static_cast<const uint16_t*>(a.w), static_cast<const uint16_t*>(a.bias), a.res,
+                 static_cast<uint16_t*>(a.y)};
+    // K parts: 16 to 32 warps an SM, each with two steps or more (one token, 2048 -> 7168: 11.0
+    // us with 12, 7.9 us with 24, 8.7 us with 48, in a second wave)
+    const int64_t warps = (a.N + kOut - 1) / kOut;
+    const int steps = (a.K + 255) / 256;
+    while (p.parts < kVecWarps && warps * p.parts < (int64_t)16 * a.num_ctas && p.parts * 2 <= steps) p.parts *= 2;
+    const int per = kVecWarps / p.parts * kOut;
+    return launch_pdl(linear_vec_kernel<F16, GLU, NT>, dim3((unsigned)((a.N + per - 1) / per)), dim3(32 * kVecWarps), 0,
+                      s, p);
+}
+template <bool F16, bool GLU>
+cudaError_t launch_vec_n(const LinearArgs& a, cudaStream_t s) {
+    return a.T == 1 ? launch_vec<F16, GLU, 1>(a, s) : a.T == 2 ? launch_vec<F16, GLU, 2>(a, s) : launch_vec<F16, GLU, 4>(a, s);
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+    const bool glu = a.act == MOE_ACT_SWIGLU;
+    // The vector kernel saves the tile kernel's fixed steps; its loads come nearer to HBM's rate
+    // the fewer tokens share the registers.  Measured (vector against tile kernel, us): one
+    // token 2 MB of weights 2.1 / 4.1, 17 MB 4.8 / 7.1, 29 MB 7.9 / 9.4, 59 MB 11.3 / 12.7, 76 MB
+    // 17.0 / 15.7, 134 MB 26.1 / 23.7; four tokens 2 MB 3.2 / 4.2, 8 MB 5.5 / 6.1, 17 MB 7.7 / 7.5.
+    const int64_t bytes = (int64_t)2 * a.K * a.N * (glu ? 2 : 1);
+    if (bytes <= (a.T == 1 ? (int64_t)64 << 20 : a.T <= kVecTok ? (int64_t)12 << 20 : 0)) {
+        if (glu) return a.f16 ? launch_vec_n<true, true>(a, s) : launch_vec_n<false, true>(a, s);
+        return a.f16 ? launch_vec_n<true, false>(a, s) : launch_vec_n<false, false>(a, s);
+    }
     if (a.T >= 512) {
         if (a.act == MOE_ACT_SWIGLU) return a.f16 ? launch_pair<true, true>(a, s) : launch_pair<false, true>(a, s);
         return a.f16 ? launch_pair<true, false>(a, s) : launch_pair<false, false>(a, s);

@@ -138,6 +138,15 @@ def test_larger(T, K, N, act):
     run(T, K, N, act, "bf16", seed=T + N, residual="same", pad=16)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("act", [0, 5])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("K,N", [(1, 1), (255, 3), (256, 5), (257, 9), (2048, 33), (3001, 700), (6000, 5), (1100, 4001),
+                                 (9000, 4100)])
+def test_a_few_tokens(K, N, T, act, dtype):
+    run(T, K, N, act, dtype, residual="f32" if N % 2 else "same", seed=K + T, pad=8 * (T % 2))
+
+
 @pytest.mark.parametrize("T", [1, 40, 700])
 def test_in_place_residual_and_column_slices(T):
     """The residual stream updated in place, x and y being column slices of one buffer."""
@@ -224,7 +233,7 @@ def test_empty_batch_is_a_no_op():
     moe.moe_linear(x, w, torch.empty((0, 8), dtype=torch.bfloat16, device="cuda"), _ws())
 
 
-@pytest.mark.parametrize("T", [1, 300, 2000])
+@pytest.mark.parametrize("T", [20, 300, 2000])              # up to four tokens nothing waits
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(T):
     import torch
     moe = _moe()
