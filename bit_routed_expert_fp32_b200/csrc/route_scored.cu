@@ -174,7 +174,7 @@ __device__ __noinline__ int choose_careful(const ScoreArgs& r, int E, int k, Scr
 // Order-preserving 32-bit key of a value that is not NaN (0 is below every key) and back.
 __device__ inline uint32_t key32(float f) {
     const uint32_t b = __float_as_uint(f + 0.f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ inline float unkey32(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k); }
 
@@ -218,17 +218,18 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
             for (int j = 0; j < 8; ++j) c[j] = c[j] * iz + b[j];
         }
     }
-    bool fine = true;
+    // NaN anywhere, or opposite infinities in a lane, make a lane's sum NaN
+    float sum = 0.f;
     uint32_t key[8];
+    const int live = E - 8 * lane;                         // experts of this lane (or more)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const bool in = 8 * lane + j < E;
         const float v = by_logit ? L[j] : c[j];
-        fine &= !in || v == v;
-        if (grouped) fine &= !in || c[j] == c[j];
+        const bool in = j < live;
+        if (in) sum += by_logit && grouped ? v + c[j] : v;
         key[j] = in ? (key32(v) & ~7u) | (7u - j) : 0u;
     }
-    if (!__all_sync(0xffffffffu, fine)) return false;
+    if (__any_sync(0xffffffffu, sum != sum)) return false;
     if (grouped) {
         const int gs = E / r.n_groups, lpg = gs >> 3;
         float t1, t2;
@@ -265,23 +266,30 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
             }
             leader = 1;
         }
+        // the best groups one by one; lanes past the last group hold none
         const float sc = r.group_top == 2 ? t1 + t2 : t1;
-        const int mine = lane / leader;
-        int rank = 0;
-        for (int g = 0; g < r.n_groups; ++g) {
-            const float o = __shfl_sync(0xffffffffu, sc, g * leader);
-            rank += o > sc || (o == sc && g < mine);
+        uint32_t rest = lane < r.n_groups * leader ? key32(sc) : 0u, lo = 0;
+        if (__any_sync(0xffffffffu, rest != 0 && sc != sc)) return false;
+        unsigned lanes = 0;
+        for (int n = 0; n < r.top_groups; ++n) {
+            lo = __reduce_max_sync(0xffffffffu, rest);
+            const bool hit = rest == lo;
+            lanes |= __ballot_sync(0xffffffffu, hit);
+            if (hit) rest = 0;
         }
-        const bool in = mine < r.n_groups, keep = in && rank < r.top_groups;
-        const unsigned lanes = __ballot_sync(0xffffffffu, keep);
-        const float lo = unkey32(__reduce_min_sync(0xffffffffu, keep && sc == sc ? key32(sc) : 0xFF800000u));
-        const float hi = unkey32(__reduce_max_sync(0xffffffffu, in && !keep ? key32(sc) : 0x007FFFFFu));
-        if (__any_sync(0xffffffffu, in && sc != sc) || !(lo - hi > 2.f * abs_err + kRel * (fabsf(lo) + fabsf(hi))))
+        const float flo = unkey32(lo), fhi = unkey32(__reduce_max_sync(0xffffffffu, rest));
+        // groups that tie, and infinities, are left to fp64
+        if (__popc(lanes) != r.top_groups * leader ||
+            !(flo - fhi > 2.f * abs_err + kRel * (fabsf(flo) + fabsf(fhi))))
             return false;
+        if (leader > 1 || gs == 8) {                       // a lane's experts are of one group
+            if (!((lanes >> lane) & 1u))
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int g = leader == 1 ? (8 * lane + j) / gs : mine;
-            if (!((lanes >> (g * leader)) & 1u)) key[j] = 0;
+                for (int j = 0; j < 8; ++j) key[j] = 0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (j < live && !((lanes >> ((8 * lane + j) / gs)) & 1u)) key[j] = 0;
         }
     }
     // descending, by the 19 comparators of Batcher's odd-even merge sort
@@ -294,6 +302,7 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
         key[B[q]] = min(x, y);
     }
     uint32_t mine = 0;                                     // lane n: the n-th largest key
+    int from = 0;                                          // and the lane it was in
     for (int n = 0; n <= k; ++n) {
         const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
         const int wl = __ffs(__ballot_sync(0xffffffffu, key[0] == top)) - 1;
@@ -304,9 +313,10 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
         }
         if (lane == n) {
             mine = top;
-            my_id = 8 * wl + 7 - (int)(top & 7u);
+            from = wl;
         }
     }
+    my_id = 8 * from + 7 - (int)(mine & 7u);
     const float v = unkey32(mine & ~7u);
     const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1);
     bool ok = true;

@@ -24,7 +24,6 @@ using namespace tc5;
 
 constexpr int kDrain = 2;                  // stages per accumulator
 constexpr int kThreads = 384, kTok = 256, kMaxStages = 6, kEpiWarps = 8;
-constexpr int kAhead = 6;                  // stages between a token box's L2 prefetch and its load
 
 struct LogitArgs {
     int T, H, E;
@@ -99,7 +98,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bar = map_peer(smem_u32(&S.full[slot]), crank & ~1);
                 if (rank == 0) mbar_arrive_expect_tx(&S.full[slot], 2 * stage_bytes);
                 tma_load_2d_pair(dst, &xmap, (kc0 + i) * kBK, t0, bar);
-                if (kAhead && i + kAhead < n_stage) tma_prefetch_2d(&xmap, (kc0 + i + kAhead) * kBK, t0);
 #pragma unroll
                 for (int pl = 0; pl < 3; ++pl)
                     tma_load_2d_pair(dst + xbytes + pl * wbytes, &wmap, (kc0 + i) * kBK,
@@ -243,12 +241,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
-// An MMA takes the tensor core 128 clocks however few columns it has (the pair kernel's twelve
-// per stage take 1536 at 64 experts as at 256), so with few tokens, or few experts, the
-// weights are the rows instead: the three planes of 40 experts stacked, D[3 x 40][tokens] =
-// planes x^T, four MMAs a stage by single CTAs, K over a cluster; accumulators, the adding
-// warps and the joining of parts as in the pair kernel, and the planes are joined there too.
-// (130 tokens of the full-size layer, whole call: 30.7 us by pairs, 25.2 us so.)
+// With few tokens, or few experts, most of a pair's tile would be empty and its token boxes
+// read for few columns, so the weights are the rows instead: the three planes of 40 experts
+// stacked, D[3 x 40][tokens] = planes x^T, four MMAs a stage by single CTAs, K over a cluster;
+// accumulators, the adding warps and the joining of parts as in the pair kernel, and the
+// planes are joined there too.  (130 tokens of the full-size layer, whole call: 30.7 us by
+// pairs, 25.2 us so.)
 constexpr int kExp = 40, kFewSplit = 8;
 constexpr uint32_t kPlanesBytes = 128 * kBK * 2;          // 120 rows, and eight that nothing reads
 
