@@ -57,8 +57,21 @@ __device__ inline float apply_act(int act, float a) {
     switch (act) {
         case MOE_ACT_RELU: return a > 0.f || a != a ? a : 0.f;      // NaN stays NaN
         case MOE_ACT_SILU: return silu_fast(a);
-        case MOE_ACT_GELU: return 0.5f * a * (1.f + erff(a * 0.70710678f));
-        case MOE_ACT_GELU_TANH: return 0.5f * a * (1.f + tanhf(0.79788456f * (a + 0.044715f * a * a * a)));
+        case MOE_ACT_GELU: {
+            // a Phi(a), Phi(-|a|) = erfc(|a| / sqrt 2) / 2 by Abramowitz and Stegun 7.1.26 (off by
+            // at most 7.5e-8, a fifth of the instructions of erfcf)
+            const float x = fabsf(a) * 0.70710678f, t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+            const float poly =
+                t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                         0.254829592f);
+            const float q = 0.5f * poly * __expf(-x * x);
+            return a != a ? a : a * (a < 0.f ? q : 1.f - q);
+        }
+        case MOE_ACT_GELU_TANH: {
+            // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
+            const float z2 = 1.59576912f * (a + 0.044715f * a * a * a);
+            return __fdividef(a, 1.f + __expf(-z2));
+        }
     }
     return a;
 }
@@ -143,6 +156,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     extern __shared__ uint8_t smem_raw[];
     __shared__ LinShared S;
     constexpr int kOut = GLU ? kFeat / 2 : kFeat;       // outputs per tile
+    constexpr int kPer = kLinThreads / (kOut / 4);      // tokens a CTA forms at a time, four outputs a thread
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = p.split > 1 ? (int)cluster_rank() : 0;
@@ -234,6 +248,25 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         }
         if (elect_one()) umma_commit(&S.done);          // every MMA issued has completed
         __syncwarp();
+    } else {
+        // the bias, and the residual rows of this CTA's share of the tile (kPer tokens of every
+        // split * kPer, see below), on their way to L2 meanwhile
+        const int width = min(kOut, p.N - f0), id = threadIdx.x - 64;
+        if (p.bias && id < 2 * kOut / 64) {
+            const int j = id % (kOut / 64);
+            prefetch_l2(static_cast<const uint16_t*>(p.bias) + (GLU ? id / (kOut / 64) * p.N : 0) + f0 +
+                        min(64 * j, width - 1));
+        }
+        if (p.res) {
+            const int rsize = p.res_f32 ? 4 : 2, lines = (width * rsize + 254) / 128;
+            for (int i = id;; i += kLinThreads - 64) {
+                const int j = i / lines, tok = (part + p.split * (j / kPer)) * kPer + j % kPer;
+                if (tok - j % kPer >= ntok) break;
+                if (tok < ntok)
+                    prefetch_l2(static_cast<const uint8_t*>(p.res) + ((int64_t)(t0 + tok) * p.ldr + f0) * rsize +
+                                min((i - j * lines) * 128, width * rsize - 1));
+            }
+        }
     }
     if (!mbar_wait_bounded(&S.done, 0, kWaitLimit)) {
         st_volatile(S.abort_flag, 1);
@@ -285,13 +318,13 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         for (int i = part * kLinThreads + threadIdx.x; i < ntok * (kOut / 4); i += p.split * kLinThreads) {
             const int tok = i / (kOut / 4), f = 4 * (i % (kOut / 4)), n = f0 + f;
             if (n >= p.N) continue;
-            float a[4], u[4];
-            total(tok * kFeat + f, a);
-            if (GLU) total(tok * kFeat + kOut + f, u);
             const int64_t t = t0 + tok;
             float o[4], res[4] = {0.f, 0.f, 0.f, 0.f};
             const bool full = n + 3 < p.N;
             if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + n, p.N - n, res);
+            float a[4], u[4];
+            total(tok * kFeat + f, a);
+            if (GLU) total(tok * kFeat + kOut + f, u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 float v = a[j];

@@ -159,6 +159,9 @@ __device__ inline float4 ld_peer_v4(uint32_t addr) {
     return v;
 }
 
+// The line of p into L2.
+__device__ inline void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---- waits ---------------------------------------------------------------------------------
 __device__ inline int ld_volatile(const int& v) { return *reinterpret_cast<const volatile int*>(&v); }
 __device__ inline void st_volatile(int& v, int x) { *reinterpret_cast<volatile int*>(&v) = x; }
