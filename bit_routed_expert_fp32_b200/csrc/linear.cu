@@ -49,6 +49,30 @@ __device__ inline uint16_t from_f32(float v) {
     return F16 ? f32_to_f16_bits(v) : f32_to_bf16_bits(v);
 }
 
+template <bool F16>
+__device__ inline void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (F16) {
+            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            f[2 * j] = p.x;
+            f[2 * j + 1] = p.y;
+        } else {
+            f[2 * j] = __uint_as_float(u[j] << 16);
+            f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+    }
+}
+// Two values rounded, the first in the low half.
+template <bool F16>
+__device__ inline uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // silu with the fast exponential and quotient: relative error about 1e-6, far below the
 // 16-bit rounding of the output
 __device__ inline float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
@@ -446,13 +470,14 @@ struct PairArgs {
     const void* bias;
     const void* res;
     void* y;
-    int vec;                 // 4 consecutive values of a row of y can be written at once
+    int vec, vec8;           // 4 / 8 consecutive values of a row of y can be written at once
     int vec_res;             // 4 consecutive residual values can be read at once
+    int vec_bias;            // 8 consecutive bias values can be read at once
     Ctrl* ctrl;
 };
 
 struct PairShared {
-    uint64_t full[kPairStages], empty_[kPairStages], acc_full[2], acc_empty[2], drained, stall_bar;
+    uint64_t full[kPairStages], empty_[kPairStages], acc_full[2], acc_empty[2], peer_ready, drained, stall_bar;
     uint32_t tmem;
     int abort_flag;
 };
@@ -488,19 +513,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             mbar_init(&S.acc_full[i], 1);
             mbar_init(&S.acc_empty[i], 2 * kPairEpi);    // the epilogue warps of both CTAs
         }
+        mbar_init(&S.peer_ready, 1);
         mbar_init(&S.drained, 1);
         mbar_init(&S.stall_bar, 1);                     // nothing ever arrives on it
         fence_mbar_init();
         S.abort_flag = 0;
     }
-    griddep_wait();
-    if (warp == 2) tmem_alloc_pair(&S.tmem, kPairCols);
-    fence_before();
     __syncthreads();
-    cluster_sync();
-    fence_after();
-    griddep_launch_dependents();
-    const uint32_t tmem = S.tmem;
+    cluster_sync();                                     // both CTAs' barriers exist
+    griddep_wait();
+    if (warp == 2) {
+        tmem_alloc_pair(&S.tmem, kPairCols);
+        // the leader's MMAs write both CTAs' columns
+        if (rank == 1 && lane == 0) mbar_arrive_peer(map_peer(smem_u32(&S.peer_ready), 0));
+        __syncwarp();
+    }
+    if (warp != 0 && warp != 3) {                       // all but the producer, which needs no columns
+        fence_before();
+        named_bar_sync(1, kPairThreads - 64);
+        fence_after();
+        griddep_launch_dependents();
+    }
 
     if (warp == 0) {
         // ---- producer: this CTA's rows, counted on the leader's barrier -----------------
@@ -536,6 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         // ---- MMA issuer (the leader's) ----------------------------------------------------
+        const uint32_t tmem = S.tmem;
         constexpr uint32_t idesc = instr_desc(F16, 256, 256);
         const uint64_t ad0 = smem_desc(smem_u32(smem)), bd0 = smem_desc(smem_u32(smem) + 128 * kBK * 2);
         const uint32_t stall = p.ctrl->test_stall;
@@ -550,6 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         }
+        if (ok) ok = __all_sync(0xffffffffu, pair_wait(S.abort_flag, &S.peer_ready, 0, p.ctrl, kDetWaitFull | 0x64));
         int slot = 0, n = 0;
         uint32_t par = 0;
         for (int tile = pair; tile < n_tiles && ok; tile += n_pairs, ++n) {
@@ -578,8 +613,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (ok && elect_one()) umma_commit_pair(&S.acc_full[buf]);
             __syncwarp();
         }
-        if (elect_one()) umma_commit_pair(&S.drained);
-        __syncwarp();
+        // The last tile's accumulator was full before anyone leaves; after an abort, what was
+        // issued must end here.
+        if (!ok) {
+            if (elect_one()) umma_commit_pair(&S.drained, 1);
+            __syncwarp();
+            if (!mbar_wait_bounded(&S.drained, 0, kWaitLimit)) report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetDrain | 0x63);
+            __syncwarp();
+        }
     } else if (warp >= 4) {
         // ---- epilogue -----------------------------------------------------------------
         const int q = warp & 3, half = (warp - 4) >> 2;   // tensor-memory lanes 32q .. 32q+31; columns
@@ -595,6 +636,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const int t0 = tt * kPairTok + rank * 128 + 32 * q, nb = ft * kOut + half * kCols;
             // whole tiles with aligned rows move four values at a time without checks
             const bool whole = t0 + 32 <= p.T && nb + kCols <= p.N && p.vec && (!p.res || p.vec_res);
+            // without a residual the values are rounded before they change lanes: half the bytes
+            const bool packed = whole && p.vec8 && !p.res && (!p.bias || p.vec_bias);
             uint4 rbuf[8];
             auto load_res = [&](int c0) {
                 const int64_t at = (int64_t)(t0 + lr) * p.ldr + nb + c0 + 4 * c4;
@@ -617,7 +660,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                             pair_wait(S.abort_flag, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
                 break;
             fence_after();
-            const uint32_t tl = tmem + buf * 256 + half * kCols + ((uint32_t)(32 * q) << 16);
+            const uint32_t tl = S.tmem + buf * 256 + half * kCols + ((uint32_t)(32 * q) << 16);
 #pragma unroll 1
             for (int c0 = 0; c0 < kCols; c0 += 32) {
                 const int n0 = nb + c0, nc = n0 + 4 * c4;
@@ -642,6 +685,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         v[j] = __float_as_uint(silu_fast(__uint_as_float(v[j])) * __uint_as_float(u[j]));
+                }
+                if (packed) {
+                    if (!GLU) {
+                        if (p.bias) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float b[8];
+                                unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n0) + j), b);
+#pragma unroll
+                                for (int u = 0; u < 8; ++u)
+                                    v[8 * j + u] = __float_as_uint(__uint_as_float(v[8 * j + u]) + b[u]);
+                            }
+                        }
+                        float o[8][4];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j >> 2][j & 3] = __uint_as_float(v[j]);
+                        apply_act_all(p.act, o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(o[j >> 2][j & 3]);
+                    }
+                    uint4* const sp = reinterpret_cast<uint4*>(sq);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            w[u] = pack2<F16>(__uint_as_float(v[8 * j + 2 * u]), __uint_as_float(v[8 * j + 2 * u + 1]));
+                        sp[lane * 4 + (j ^ ((lane >> 1) & 3))] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    __syncwarp();
+                    uint16_t* yp = static_cast<uint16_t*>(p.y) + (int64_t)(t0 + (lane >> 2)) * p.ldy + n0 + 8 * (lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2);
+                        *reinterpret_cast<uint4*>(yp + 8 * i * p.ldy) = sp[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                    }
+                    continue;
                 }
                 __syncwarp();
 #pragma unroll
@@ -715,13 +796,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
     fence_before();
     __syncthreads();
-    // every MMA issued has completed (the commit arrives in both CTAs)
-    if (warp == 1 && !mbar_wait_bounded(&S.drained, 0, kWaitLimit))
-        report_error(p.ctrl, MOE_ERR_TIMEOUT, kDetDrain | 0x63);
-    __syncwarp();
     cluster_sync();                     // both CTAs are done with each other's memory
     fence_after();
-    if (warp == 2) tmem_dealloc_pair(tmem, kPairCols);
+    if (warp == 2) tmem_dealloc_pair(S.tmem, kPairCols);
 }
 
 template <bool F16, bool GLU>
@@ -740,7 +817,9 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t s) {
     p.y = a.y;
     p.ctrl = a.ctrl;
     p.vec = vec4_ok(a.y, a.ldy, 2);
+    p.vec8 = a.ldy % 8 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
     p.vec_res = vec4_ok(a.res, a.ldr, a.res_f32 ? 4 : 2);
+    p.vec_bias = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0 && (!GLU || a.N % 8 == 0);
     p.ttiles = (a.T + kPairTok - 1) / kPairTok;
     p.ftiles = (a.N + kOut - 1) / kOut;
     p.group = 8;
@@ -772,21 +851,6 @@ struct VecArgs {
     uint16_t* y;
 };
 
-template <bool F16>
-__device__ inline void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (F16) {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-            f[2 * j] = p.x;
-            f[2 * j + 1] = p.y;
-        } else {
-            f[2 * j] = __uint_as_float(u[j] << 16);
-            f[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-    }
-}
 // 16 bytes that are read once (they stay out of L1).
 __device__ inline uint4 ld_stream(const void* p) {
     uint4 r;
