@@ -370,8 +370,60 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     if (p.split > 1) cluster_sync();
 }
 
+// How the tile kernel runs a product, and the clocks that is estimated to take.
+struct TilePlan {
+    int nt, ttiles, ftiles, split, stages;
+    uint32_t tmem_cols;
+    size_t smem;
+    double clocks;
+};
+
+TilePlan plan_tiles(const LinearArgs& a) {
+    const bool glu = a.act == MOE_ACT_SWIGLU;
+    const int chunks = (a.K + kBK - 1) / kBK, out = glu ? kFeat / 2 : kFeat;
+    TilePlan best = {};
+    // Tiles of at most 128 tokens (one of up to 160 where that is all of them): tensor memory
+    // and shared memory then let two CTAs share an SM.
+    best.ttiles = a.T <= 160 ? 1 : (a.T + 127) / 128;
+    best.nt = (int)(((int64_t)a.T + best.ttiles - 1) / best.ttiles + 15) & ~15;
+    best.ftiles = (a.N - 1) / out + 1;
+    best.tmem_cols = 32;
+    while ((int)best.tmem_cols < best.nt) best.tmem_cols *= 2;
+    const int64_t tiles = (int64_t)best.ftiles * best.ttiles;
+    const int stage_bytes = kTileBytes + best.nt * kBK * 2;
+    for (int split = 1; split <= kMaxSplit && (split == 1 || split * 2 <= chunks); ++split) {
+        TilePlan p = best;
+        // stages: four, or as many as two CTAs on an SM leave room for
+        const int fit = p.nt <= 128 ? 112 * 1024 / stage_bytes : 4, per = (chunks + split - 1) / split;
+        p.split = split;
+        p.stages = fit < 4 ? fit : 4;
+        if (p.stages > per) p.stages = per;
+        p.smem = (size_t)p.stages * stage_bytes;
+        const size_t sums = (size_t)p.nt * kFeat * 4;
+        if (p.smem < sums) p.smem = sums;
+        if (p.smem < tmem_smem(p.tmem_cols)) p.smem = tmem_smem(p.tmem_cols);
+        p.smem += 1024;
+        int per_sm = (int)(228 * 1024 / (p.smem + 1024 + sizeof(LinShared)));
+        per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
+        // The stages' bytes come at the 64 a clock that L2 gives an SM, if there are enough of them
+        // in flight for some 2400 clocks; the sums of a token of the tile take some 45 clocks; a
+        // wave some 10600 beside that (launch, first load, barriers).  (One token, 2048 -> 7168:
+        // 13.1 us with one part, 9.9 with two, 9.0 with four or five, 9.2 with six, 12.5 with
+        // eight, in a second wave; 384 tokens, 4096 -> 4096: 23.3 us with two, 32.5 with three,
+        // whose 96 clusters do not fit at once.)
+        const int64_t cap = (int64_t)cluster_capacity(split, per_sm, a.num_ctas);
+        const int64_t waves = (tiles + cap - 1) / cap, ctas = tiles * split;
+        const int64_t share = ctas <= a.num_ctas ? 1 : per_sm;
+        const double flight = (double)share * p.stages * stage_bytes / 2400.0, rate = flight < 64.0 ? flight : 64.0;
+        p.clocks = (double)waves * (share * per * (stage_bytes / rate) + 10600.0 + 45.0 * p.nt);
+        // more parts where it makes no difference: less is left to each CTA's first load
+        if (best.split == 0 || p.clocks <= 1.02 * best.clocks) best = p;
+    }
+    return best;
+}
+
 template <bool F16, bool GLU>
-cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
+cudaError_t launch(const LinearArgs& a, const TilePlan& pl, cudaStream_t s) {
     constexpr int kOut = GLU ? kFeat / 2 : kFeat;
     LinKernelArgs p = {};
     p.T = a.T;
@@ -379,6 +431,11 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
     p.K = a.K;
     p.act = a.act;
     p.res_f32 = a.res_f32;
+    p.nt = pl.nt;
+    p.ftiles = pl.ftiles;
+    p.split = pl.split;
+    p.stages = pl.stages;
+    p.tmem_cols = pl.tmem_cols;
     p.ldr = a.ldr;
     p.ldy = a.ldy;
     p.bias = a.bias;
@@ -387,52 +444,18 @@ cudaError_t launch(const LinearArgs& a, cudaStream_t s) {
     p.ctrl = a.ctrl;
     p.vec = vec4_ok(a.y, a.ldy, 2);
     p.vec_res = vec4_ok(a.res, a.ldr, a.res_f32 ? 4 : 2);
-    // Tiles of at most 128 tokens (one of up to 160 where that is all of them): tensor memory
-    // and shared memory then let two CTAs share an SM.  Stages: four, or as many as that
-    // leaves room for.
-    const int ttiles = a.T <= 160 ? 1 : (a.T + 127) / 128;
-    p.nt = ((a.T + ttiles - 1) / ttiles + 15) & ~15;
-    p.tmem_cols = 32;
-    while ((int)p.tmem_cols < p.nt) p.tmem_cols *= 2;
-    p.ftiles = (a.N + kOut - 1) / kOut;
-    const int chunks = (a.K + kBK - 1) / kBK;
-    const int64_t tiles = (int64_t)p.ftiles * ttiles;
-    const int stage_bytes = kTileBytes + p.nt * kBK * 2;
-    size_t smem = 0;
-    auto plan = [&](int split) {                        // -> CTAs that are resident at once
-        const int fit = p.nt <= 128 ? 112 * 1024 / stage_bytes : 4, per = (chunks + split - 1) / split;
-        p.split = split;
-        p.stages = fit < 4 ? fit : 4;
-        if (p.stages > per) p.stages = per;
-        smem = (size_t)p.stages * stage_bytes;
-        const size_t sums = (size_t)p.nt * kFeat * 4;
-        if (smem < sums) smem = sums;
-        if (smem < tmem_smem(p.tmem_cols)) smem = tmem_smem(p.tmem_cols);
-        smem += 1024;
-        return a.num_ctas * (int64_t)(228 * 1024 / (smem + 1024 + sizeof(LinShared)));
-    };
-    // K parts: as many as leave every CTA two stages or more of work and all CTAs resident at
-    // once, at most two on an SM (one token, 2048 -> 7168: 13.1 us with one part, 9.9 with
-    // two, 9.0 with four or five, 9.2 with six, 12.5 with eight, in a second wave).
-    plan(1);
-    for (int split = 2; split <= kMaxSplit && split * 2 <= chunks; ++split) {
-        const int64_t slots = plan(split);
-        if (tiles * split > slots || tiles * split > 2 * a.num_ctas) {
-            plan(split - 1);
-            break;
-        }
-    }
+    const int64_t ctas = (int64_t)pl.ftiles * pl.ttiles * pl.split;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     CUtensorMap wm, xm;
     if (!make_map(&wm, F16, a.w, (int64_t)(GLU ? 2 : 1) * a.N, a.K, a.ldw, kOut) ||
         !make_map(&xm, F16, a.x, a.T, a.K, a.ldx, p.nt))
         return cudaErrorInvalidConfiguration;
-    if (tiles * p.split > INT32_MAX) return cudaErrorInvalidConfiguration;
-    cudaError_t err = set_smem_limit(linear_kernel<F16, GLU>, smem);
+    cudaError_t err = set_smem_limit(linear_kernel<F16, GLU>, pl.smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.split));
+    cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(kLinThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -634,25 +657,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             pair_tile(p, tile, tt, ft);
             const int buf = n & 1;
             const int t0 = tt * kPairTok + rank * 128 + 32 * q, nb = ft * kOut + half * kCols;
-            // whole tiles with aligned rows move four values at a time without checks
-            const bool whole = t0 + 32 <= p.T && nb + kCols <= p.N && p.vec && (!p.res || p.vec_res);
+            // whole columns in aligned rows move four values at a time; rows past the last token
+            // read its residual and are not written
+            const bool whole = t0 < p.T && nb + kCols <= p.N && p.vec && (!p.res || p.vec_res);
+            const int left = p.T - t0;
             // without a residual the values are rounded before they change lanes: half the bytes
             const bool packed = whole && p.vec8 && !p.res && (!p.bias || p.vec_bias);
             uint4 rbuf[8];
             auto load_res = [&](int c0) {
-                const int64_t at = (int64_t)(t0 + lr) * p.ldr + nb + c0 + 4 * c4;
+                const int64_t at = (int64_t)t0 * p.ldr + nb + c0 + 4 * c4;
                 if (res16) {
                     const uint16_t* src = static_cast<const uint16_t*>(p.res) + at;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const uint2 v = *reinterpret_cast<const uint2*>(src + 4 * i * p.ldr);
+                        const uint2 v = *reinterpret_cast<const uint2*>(src + min(4 * i + lr, left - 1) * p.ldr);
                         rbuf[i].x = v.x;
                         rbuf[i].y = v.y;
                     }
                 } else {
                     const float* src = static_cast<const float*>(p.res) + at;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) rbuf[i] = *reinterpret_cast<const uint4*>(src + 4 * i * p.ldr);
+                    for (int i = 0; i < 8; ++i)
+                        rbuf[i] = *reinterpret_cast<const uint4*>(src + min(4 * i + lr, left - 1) * p.ldr);
                 }
             };
             if (whole && p.res) load_res(0);
@@ -720,7 +746,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 8 * i + (lane >> 2);
-                        *reinterpret_cast<uint4*>(yp + 8 * i * p.ldy) = sp[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
+                        if (r < left)
+                            *reinterpret_cast<uint4*>(yp + 8 * i * p.ldy) = sp[r * 4 + ((lane & 3) ^ ((r >> 1) & 3))];
                     }
                     continue;
                 }
@@ -773,7 +800,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         if (c0 + 32 < kCols) load_res(c0 + 32);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) store4<F16>(yp + 4 * i * p.ldy, true, 4, o[i]);
+                    for (int i = 0; i < 8; ++i)
+                        if (4 * i + lr < left) store4<F16>(yp + 4 * i * p.ldy, true, 4, o[i]);
                 } else if (nc < p.N) {
                     const bool full = nc + 3 < p.N;
 #pragma unroll
@@ -999,12 +1027,18 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
         if (glu) return a.f16 ? launch_vec_n<true, true>(a, s) : launch_vec_n<false, true>(a, s);
         return a.f16 ? launch_vec_n<true, false>(a, s) : launch_vec_n<false, false>(a, s);
     }
-    if (a.T >= 512) {
-        if (a.act == MOE_ACT_SWIGLU) return a.f16 ? launch_pair<true, true>(a, s) : launch_pair<false, true>(a, s);
+    // A pair's stage takes its MMAs (512 clocks, 545 measured), a wave of pairs some 13000 beside
+    // its tiles.  (4096 -> 4096, tile against pair kernel, us: 130 tokens 14.6 / 25.2, 256 16.8 /
+    // 25.4, 512 24.0 / 24.8, 768 40.5 / 27.3; 512 -> 8192: 130 tokens 11.7 / 9.8.)
+    const TilePlan pl = plan_tiles(a);
+    const int64_t ptiles = (int64_t)((a.T - 1) / kPairTok + 1) * ((a.N - 1) / (glu ? 128 : 256) + 1);
+    const int64_t waves = (ptiles + a.num_ctas / 2 - 1) / (a.num_ctas / 2);
+    if (13000.0 + (double)waves * ((a.K + kBK - 1) / kBK) * 545.0 < pl.clocks) {
+        if (glu) return a.f16 ? launch_pair<true, true>(a, s) : launch_pair<false, true>(a, s);
         return a.f16 ? launch_pair<true, false>(a, s) : launch_pair<false, false>(a, s);
     }
-    if (a.act == MOE_ACT_SWIGLU) return a.f16 ? launch<true, true>(a, s) : launch<false, true>(a, s);
-    return a.f16 ? launch<true, false>(a, s) : launch<false, false>(a, s);
+    if (glu) return a.f16 ? launch<true, true>(a, pl, s) : launch<false, true>(a, pl, s);
+    return a.f16 ? launch<true, false>(a, pl, s) : launch<false, false>(a, pl, s);
 }
 
 }  // namespace moe
