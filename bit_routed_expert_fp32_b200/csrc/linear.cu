@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
         for (int c = 16 * (warp >> 2); c < ntok; c += 32) {
             uint32_t v[16];
             tmem_ld16(tl + c, v);
-            ld_wait();
+            ld_wait(v);
 #pragma unroll
             for (int u = 0; u < 16; ++u) sums[(size_t)(c + u) * kFeat + (threadIdx.x & 127)] = __uint_as_float(v[u]);
         }
@@ -665,8 +665,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const bool packed = whole && p.vec8 && !p.res && (!p.bias || p.vec_bias);
             uint4 rbuf[8];
             auto load_res = [&](int c0) {
-                const int64_t at = (int64_t)t0 * p.ldr + nb + c0 + 4 * c4;
-                if (res16) {
+                const int n = nb + c0 + 4 * c4;
+                const int64_t at = (int64_t)t0 * p.ldr + n;
+                if (!whole) {
+                    // odd strides, or the last columns: value by value, as fp32 (columns past the
+                    // last read the last one's)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int64_t ri = at + min(4 * i + lr, left - 1) * p.ldr;
+                        float f[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int64_t k = ri + min(j, p.N - 1 - n);
+                            f[j] = res16 ? to_f32<F16>(static_cast<const uint16_t*>(p.res)[k])
+                                         : static_cast<const float*>(p.res)[k];
+                        }
+                        rbuf[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                             __float_as_uint(f[3]));
+                    }
+                } else if (res16) {
                     const uint16_t* src = static_cast<const uint16_t*>(p.res) + at;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -681,7 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         rbuf[i] = *reinterpret_cast<const uint4*>(src + min(4 * i + lr, left - 1) * p.ldr);
                 }
             };
-            if (whole && p.res) load_res(0);
+            if (p.res && left > 0) load_res(0);
             if (!__all_sync(0xffffffffu,
                             pair_wait(S.abort_flag, &S.acc_full[buf], (uint32_t)(n >> 1) & 1, p.ctrl, kDetWaitFull | 0x63)))
                 break;
@@ -693,12 +710,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (n0 >= p.N) break;
                 uint32_t v[32];
                 tmem_ld32(tl + c0, v);
-                ld_wait();
+                ld_wait(v);
                 if (GLU) {
                     // both accumulators' values of an output are in one lane
                     uint32_t u[32];
                     tmem_ld32(tl + 128 + c0, u);
-                    ld_wait();
+                    ld_wait(u);
                     if (p.bias) {
                         const uint16_t* bp = static_cast<const uint16_t*>(p.bias) + n0;
 #pragma unroll
@@ -772,8 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     if (p.bias) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float b =
-                                nc + j < p.N ? to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + nc + j)) : 0.f;
+                            const float b = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + min(nc + j, p.N - 1)));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i][j] += b;
                         }
@@ -781,40 +797,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                     apply_act_all(p.act, o);
                 }
                 uint16_t* yp = static_cast<uint16_t*>(p.y) + (int64_t)(t0 + lr) * p.ldy + nc;
-                if (whole) {
-                    if (p.res) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (res16) {
-                                o[i][0] += to_f32<F16>(rbuf[i].x & 0xFFFF);
-                                o[i][1] += to_f32<F16>(rbuf[i].x >> 16);
-                                o[i][2] += to_f32<F16>(rbuf[i].y & 0xFFFF);
-                                o[i][3] += to_f32<F16>(rbuf[i].y >> 16);
-                            } else {
-                                o[i][0] += __uint_as_float(rbuf[i].x);
-                                o[i][1] += __uint_as_float(rbuf[i].y);
-                                o[i][2] += __uint_as_float(rbuf[i].z);
-                                o[i][3] += __uint_as_float(rbuf[i].w);
-                            }
-                        }
-                        if (c0 + 32 < kCols) load_res(c0 + 32);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (4 * i + lr < left) store4<F16>(yp + 4 * i * p.ldy, true, 4, o[i]);
-                } else if (nc < p.N) {
-                    const bool full = nc + 3 < p.N;
+                if (p.res && left > 0) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int64_t t = t0 + 4 * i + lr;
-                        if (t >= p.T) break;
-                        float res[4] = {0.f, 0.f, 0.f, 0.f};
-                        if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + nc, p.N - nc, res);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) o[i][j] += res[j];
-                        store4<F16>(yp + 4 * i * p.ldy, p.vec && full, p.N - nc, o[i]);
+                        if (res16 && whole) {
+                            o[i][0] += to_f32<F16>(rbuf[i].x & 0xFFFF);
+                            o[i][1] += to_f32<F16>(rbuf[i].x >> 16);
+                            o[i][2] += to_f32<F16>(rbuf[i].y & 0xFFFF);
+                            o[i][3] += to_f32<F16>(rbuf[i].y >> 16);
+                        } else {
+                            o[i][0] += __uint_as_float(rbuf[i].x);
+                            o[i][1] += __uint_as_float(rbuf[i].y);
+                            o[i][2] += __uint_as_float(rbuf[i].z);
+                            o[i][3] += __uint_as_float(rbuf[i].w);
+                        }
                     }
+                    if (c0 + 32 < kCols) load_res(c0 + 32);
                 }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (4 * i + lr < left && nc < p.N) store4<F16>(yp + 4 * i * p.ldy, whole, p.N - nc, o[i]);
             }
             fence_before();
             __syncwarp();

@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < cols) {
                     uint32_t v[16];
                     tmem_ld16(tl + c, v);
-                    ld_wait();
+                    ld_wait(v);
 #pragma unroll
                     for (int u = 0; u < 16; ++u) acc[c + u] += __uint_as_float(v[u]);
                 }
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (c < cols) {
                     uint32_t v[16];
                     tmem_ld16(tl + c, v);
-                    ld_wait();
+                    ld_wait(v);
 #pragma unroll
                     for (int u = 0; u < 16; ++u) acc[c + u] += __uint_as_float(v[u]);
                 }

@@ -133,7 +133,8 @@ def test_output_widths(T, N, act):
 
 @pytest.mark.parametrize("T,K,N,act", [(1, 7168, 2048, 5), (1, 2048, 7168, 0), (16, 7168, 4096, 2), (64, 4096, 1024, 3),
                                        (130, 1992, 4999, 4), (1000, 2048, 2048, 5), (2049, 1024, 1100, 0),
-                                       (4096, 512, 2304, 5), (3001, 712, 4100, 1), (8000, 320, 5000, 0), (5121, 136, 2600, 5)])
+                                       (4096, 512, 2304, 5), (3001, 712, 4100, 1), (8000, 320, 5000, 0), (5121, 136, 2600, 5), (3878, 187, 3155, 1),
+                                       (1030, 200, 4998, 3), (2050, 264, 1001, 5), (777, 900, 2561, 4)])
 def test_larger(T, K, N, act):
     run(T, K, N, act, "bf16", seed=T + N, residual="same", pad=16)
 
