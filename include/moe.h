@@ -218,7 +218,9 @@ moe_status moe_workspace_init(void* d_ws, size_t ws_bytes, void* stream);
  * (low byte: which kernel), then takes the path every kernel takes when one of its
  * bounded waits runs out: it issues no further copies, waits (bounded) for the copies
  * it has in flight, releases its tensor memory and returns; d_y is then unspecified.
- * cycles = 0 (or moe_workspace_init) switches the stall off.  Enqueued on stream. */
+ * cycles = 0 (or moe_workspace_init) switches the stall off.  Enqueued on stream.  The
+ * tensor-core kernels of moe_route_scored (more than 64 tokens) and of moe_linear (more than
+ * a few tokens) on this workspace take the same wait and the same path. */
 moe_status moe_workspace_set_test_stall(void* d_ws, size_t ws_bytes, uint32_t cycles, void* stream);
 
 /* Detail codes that moe_get_error returns beside MOE_ERR_TIMEOUT or
