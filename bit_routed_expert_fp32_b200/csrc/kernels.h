@@ -188,8 +188,15 @@ struct ScoreArgs {
     const float* balance;    // [E] or null: added to the scores for the choice only
 };
 cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_ctas, cudaStream_t s);
-// its logits above kSmallT tokens, from the planes in a.planes (scored_logits.cu)
-cudaError_t launch_scored_logits(const RouteArgs& a, int num_ctas, cudaStream_t s);
+// its logits above kSmallT tokens (scored_logits.cu): by single CTAs from the fp32 router (few;
+// that kernel also zeroes the n_sums span sums and the histograms), or by CTA pairs from the
+// planes in a.planes
+struct LogitPlan {
+    bool few;
+    int parts, nt, ttiles;       // K parts; tokens (few) or experts (pairs) per tile; token tiles
+};
+LogitPlan plan_scored_logits(const RouteArgs& a, int num_ctas);
+cudaError_t launch_scored_logits(const RouteArgs& a, const LogitPlan& plan, int32_t* sums, int n_sums, cudaStream_t s);
 // the decode operands (Z tables) of a.T tokens, for the decode path above kSmallT tokens
 cudaError_t launch_decode_operands(const RouteArgs& a, cudaStream_t s);
 // the routing of caller-given expert ids and gates (a.fixed_ids): histogram, scan,

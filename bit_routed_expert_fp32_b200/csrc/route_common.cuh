@@ -50,6 +50,15 @@ __device__ inline float warp_sum(float v) {
     return v;
 }
 
+// The leading bf16 pieces (the upper 16 bits) of two weights as a pair; the weights keep the
+// rest, exactly.  The 24 bits of a weight are used up by three of them.
+__device__ inline uint32_t next_plane(float& a, float& b) {
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    a -= __uint_as_float(ua & 0xFFFF0000u);
+    b -= __uint_as_float(ub & 0xFFFF0000u);
+    return __byte_perm(ua, ub, 0x7632);
+}
+
 // Exclusive scan of s_cnt[0..E) into s_off[0..E] by one warp (E <= 256).
 __device__ inline void warp_scan_counts(const int* s_cnt, int* s_off, int E, int lane) {
     int loc[8];

@@ -417,15 +417,6 @@ struct SmallSmem {
     int last;
 };
 
-// The leading bf16 pieces (the upper 16 bits) of two weights as a pair; the weights keep the
-// rest, exactly.  The 24 bits of a weight are used up by three of them.
-__device__ inline uint32_t next_plane(float& a, float& b) {
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    a -= __uint_as_float(ua & 0xFFFF0000u);
-    b -= __uint_as_float(ub & 0xFFFF0000u);
-    return __byte_perm(ua, ub, 0x7632);
-}
-
 template <int NTL, int NW>
 __global__ void __launch_bounds__(32 * NW, 2)
     scored_small_kernel(RouteArgs p, ScoreArgs r, int parts) {
@@ -797,9 +788,12 @@ cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_
     // the spans' sums and the planes take regions of the workspace that only moe_forward uses
     const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
     int32_t* sums = reinterpret_cast<int32_t*>(a.zx);
-    err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
-    if (err != cudaSuccess) return err;
-    if ((err = launch_scored_logits(a, num_ctas, s)) != cudaSuccess) return err;
+    const LogitPlan plan = plan_scored_logits(a, num_ctas);
+    if (!plan.few) {
+        err = launch_pdl(scored_split_kernel, dim3(4 * num_ctas), dim3(256), 0, s, a, a.planes, sums, n_sums);
+        if (err != cudaSuccess) return err;
+    }
+    if ((err = launch_scored_logits(a, plan, sums, n_sums, s)) != cudaSuccess) return err;
     const int top = (a.T + kTopWarps - 1) / kTopWarps;
     if ((err = launch_pdl(scored_topk_kernel, dim3(top), dim3(32 * kTopWarps), 0, s, a, r, sums)) != cudaSuccess)
         return err;

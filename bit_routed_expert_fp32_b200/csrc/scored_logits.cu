@@ -129,12 +129,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int slot = 0;
         uint32_t par = 0;
+        bool ready = false;
         for (int i = 0; i < n_stage && ok; ++i) {
             const int g = i / kDrain, buf = g & 1;
             const bool first = i % kDrain == 0, last = i % kDrain == kDrain - 1 || i == n_stage - 1;
-            ok = (!first || pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
-                                      kDetWaitEmpty | 0x71)) &&
-                 pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x70);
+            if (!ready)
+                ok = (!first || pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
+                                          kDetWaitEmpty | 0x71)) &&
+                     pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x70);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             if (ok && elect_one()) {
@@ -153,6 +155,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 slot = 0;
                 par ^= 1;
             }
+            // a wait is some 130 clocks of this warp's time: the next stage's are begun together
+            if (i + 1 == n_stage) break;
+            ready = mbar_try_wait(&S.full[slot], par);
+            if (last) ready &= mbar_try_wait(&S.acc_empty[buf ^ 1], (uint32_t)(((g + 1) >> 1) & 1) ^ 1);
         }
         if (!ok) {                                        // what was issued ends before either CTA leaves
             if (elect_one()) umma_commit_pair(&S.drained, pair_mask);
@@ -241,30 +247,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- few tokens
-// With few tokens, or few experts, most of a pair's tile would be empty and its token boxes
-// read for few columns, so the weights are the rows instead: the three planes of 40 experts
-// stacked, D[3 x 40][tokens] = planes x^T, four MMAs a stage by single CTAs, K over a cluster;
-// accumulators, the adding warps and the joining of parts as in the pair kernel, and the
-// planes are joined there too.  (130 tokens of the full-size layer, whole call: 30.7 us by
-// pairs, 25.2 us so.)
-constexpr int kExp = 40, kFewSplit = 8;
+// With few tokens, or few experts, most of a pair's tile would be empty, so the weights are the
+// rows instead: the three planes of 40 experts stacked, D[3 x 40][tokens] = planes x^T, four MMAs
+// a stage by single CTAs, K over a cluster; accumulators, the adding warps and the joining of
+// parts as in the pair kernel, and the planes are joined there too.  The planes are formed
+// here: the stage brings the fp32 rows, and a warp per stage splits them into the operand's
+// swizzled layout.  (Full-size layer, whole call: 130 tokens 24.9 us with planes written by a
+// kernel before, 21.4 us with them formed here, 34 us by pairs; 512 tokens 33.7, 29.8 and 34 us.
+// A stage takes some 960 clocks whatever its tokens, so that the pairs win from 768 tokens:
+// 2048 tokens 59 us against 76 us.)
+constexpr int kExp = 40, kFewSplit = 8, kFewStages = 5, kFewThreads = 512, kFewTok = 128;
+constexpr int kAddWarp0 = 8;                              // warps 2 .. 6 split, 8 .. 15 add
+constexpr uint32_t kRowsBytes = kExp * kBK * 4;           // fp32 rows
 constexpr uint32_t kPlanesBytes = 128 * kBK * 2;          // 120 rows, and eight that nothing reads
 
 struct FewArgs {
     int T, H, E;
-    int etiles, nt, split, stages;        // nt: tokens per tile (a multiple of 32, at most 256)
+    int etiles, nt, split;       // nt: tokens per tile (a multiple of 32, at most kFewTok)
     const float* bias;
     float* logits;
+    int32_t *hist, *sums;        // zeroed for the kernels that follow
+    int n_hist, n_sums;
     Ctrl* ctrl;
 };
 
 struct FewShared {
-    uint64_t full[kMaxStages], empty_[kMaxStages], acc_full[2], acc_empty[2], done, stall_bar;
+    uint64_t full[kFewStages], split[kFewStages], empty_[kFewStages], acc_full[2], acc_empty[2], done, stall_bar;
     uint32_t tmem;
     int abort_flag;
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kFewThreads, 1)
     scored_logits_few_kernel(const __grid_constant__ FewArgs p, const __grid_constant__ CUtensorMap xmap,
                              const __grid_constant__ CUtensorMap wmap) {
     extern __shared__ uint8_t smem_raw[];
@@ -275,15 +288,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile = blockIdx.x / p.split, tt = tile / p.etiles, e0 = (tile - tt * p.etiles) * kExp;
     const int t0 = tt * p.nt, ntok = min(p.nt, p.T - t0), chunks = p.H / kBK;
     const int kc0 = part * chunks / p.split, n_stage = (part + 1) * chunks / p.split - kc0;
-    const uint32_t stage_bytes = kPlanesBytes + (uint32_t)p.nt * kBK * 2;
-    const uint32_t load_bytes = 3 * kExp * kBK * 2 + (uint32_t)p.nt * kBK * 2;
+    // a stage: planes, tokens, fp32 rows
+    const uint32_t xbytes = (uint32_t)p.nt * kBK * 2, stage_bytes = kPlanesBytes + xbytes + kRowsBytes;
     const int groups = (n_stage + kDrain - 1) / kDrain;
 
     if (threadIdx.x == 0) {
         prefetch_map(&xmap);
         prefetch_map(&wmap);
-        for (int i = 0; i < p.stages; ++i) {
+        for (int i = 0; i < kFewStages; ++i) {
             mbar_init(&S.full[i], 1);
+            mbar_init(&S.split[i], 1);
             mbar_init(&S.empty_[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -296,38 +310,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         S.abort_flag = 0;
     }
     griddep_wait();
-    if (warp == 1) tmem_alloc(&S.tmem, 512);
+    if (warp == 1) tmem_alloc(&S.tmem, 256);
+    for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_hist; i += gridDim.x * kFewThreads) p.hist[i] = 0;
+    for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_sums; i += gridDim.x * kFewThreads) p.sums[i] = 0;
     fence_before();
     __syncthreads();
     fence_after();
     griddep_launch_dependents();
     const uint32_t tmem = S.tmem;
     const int cols = p.nt / 2;
-    float acc[128];                                       // adding warps: this row's sums of half the tokens
+    float acc[kFewTok / 2];                               // adding warps: this row's sums of half the tokens
 
     if (warp == 0) {
         int slot = 0, issued = 0;
         uint32_t par = 1;
         for (int i = 0; i < n_stage; ++i) {
-            if (!__all_sync(0xffffffffu, wait_or_flag(S.abort_flag, &S.empty_[slot], par, p.ctrl, kDetWaitEmpty | 0x72)))
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&S.empty_[slot], par) ||
+                                             wait_or_flag(S.abort_flag, &S.empty_[slot], par, p.ctrl, kDetWaitEmpty | 0x72)))
                 break;
             if (elect_one()) {
-                uint8_t* dst = smem + (size_t)slot * stage_bytes;
-                mbar_arrive_expect_tx(&S.full[slot], load_bytes);
-                tma_load_2d(dst + kPlanesBytes, &xmap, (kc0 + i) * kBK, t0, &S.full[slot]);
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl)
-                    tma_load_2d(dst + pl * kExp * kBK * 2, &wmap, (kc0 + i) * kBK, pl * p.E + e0, &S.full[slot]);
+                uint8_t* dst = smem + (size_t)slot * stage_bytes + kPlanesBytes;
+                const int k0 = (kc0 + i) * kBK;
+                mbar_arrive_expect_tx(&S.full[slot], xbytes + kRowsBytes);
+                tma_load_2d(dst + xbytes, &wmap, k0, e0, &S.full[slot]);
+                tma_load_2d(dst, &xmap, k0, t0, &S.full[slot]);
             }
             __syncwarp();
             ++issued;
-            if (++slot == p.stages) {
+            if (++slot == kFewStages) {
                 slot = 0;
                 par ^= 1;
             }
         }
         // after an abort no copy may still target shared memory at exit
-        if (lane == 0 && ld_volatile(S.abort_flag)) pair_drain(S.full, p.stages, issued, true, p.ctrl, kDetDrain | 0x72);
+        if (lane == 0 && ld_volatile(S.abort_flag)) pair_drain(S.full, kFewStages, issued, true, p.ctrl, kDetDrain | 0x72);
         __syncwarp();
     } else if (warp == 1) {
         const uint32_t idesc = instr_desc(false, 128, p.nt);
@@ -345,12 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int slot = 0;
         uint32_t par = 0;
+        bool ready = false;
         for (int i = 0; i < n_stage && ok; ++i) {
             const int g = i / kDrain, buf = g & 1;
             const bool first = i % kDrain == 0, last = i % kDrain == kDrain - 1 || i == n_stage - 1;
-            ok = (!first || wait_or_flag(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
-                                         kDetWaitEmpty | 0x73)) &&
-                 wait_or_flag(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x72);
+            // a slot that is split has its tokens too: the splitting warp waited for both
+            if (!ready)
+                ok = (!first || wait_or_flag(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
+                                             kDetWaitEmpty | 0x73)) &&
+                     wait_or_flag(S.abort_flag, &S.split[slot], par, p.ctrl, kDetWaitFull | 0x72);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             if (ok && elect_one()) {
@@ -363,27 +382,63 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (last) umma_commit(&S.acc_full[buf]);
             }
             __syncwarp();
-            if (++slot == p.stages) {
+            if (++slot == kFewStages) {
                 slot = 0;
                 par ^= 1;
             }
+            if (i + 1 == n_stage) break;                  // the next stage's waits, as above
+            ready = mbar_try_wait(&S.split[slot], par);
+            if (last) ready &= mbar_try_wait(&S.acc_empty[buf ^ 1], (uint32_t)(((g + 1) >> 1) & 1) ^ 1);
         }
         if (elect_one()) umma_commit(&S.done);          // every MMA issued has completed
         __syncwarp();
-    } else if (warp >= 4) {
-        // lanes 32 (warp % 4) .. of the tile's plane rows; half of its tokens
-        const int q = warp & 3, half = (warp - 4) >> 2;
+    } else if (warp < kAddWarp0) {
+        // A warp per slot, so that the slots' waits, reads and writes overlap (and a warp sees every
+        // phase of the barrier it waits on); eight weights at a time, one 16-byte piece of each
+        // plane's row.
+        const int slot = warp - 2;
+        for (int i = slot; i < n_stage && slot < kFewStages; i += kFewStages) {
+            const uint32_t par = (uint32_t)(i / kFewStages) & 1;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&S.full[slot], par) ||
+                                             wait_or_flag(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x75)))
+                break;
+            uint8_t* planes = smem + (size_t)slot * stage_bytes;
+            const uint8_t* rows = planes + kPlanesBytes + xbytes;
+#pragma unroll 5
+            for (int u = 0; u < kExp / 4; ++u) {
+                const int row = 4 * u + (lane >> 3), piece = lane & 7;
+                const float4* src = reinterpret_cast<const float4*>(rows + row * (kBK * 4) + piece * 32);
+                const float4 a = src[0], b = src[1];
+                float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int c = 0; c < 128; ++c) acc[c] = 0.f;
+                for (int pl = 0; pl < 3; ++pl) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[q] = next_plane(w[2 * q], w[2 * q + 1]);
+                    // the 128-byte swizzle; a plane's 40 rows are five of its 1024-byte blocks
+                    *reinterpret_cast<uint4*>(planes + pl * kExp * 128 + row * 128 + ((piece ^ (row & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.split[slot]);
+        }
+    } else {
+        // lanes 32 (warp % 4) .. of the tile's plane rows; half of its tokens
+        const int q = warp & 3, half = (warp - kAddWarp0) >> 2;
+#pragma unroll
+        for (int c = 0; c < kFewTok / 2; ++c) acc[c] = 0.f;
         for (int i = 0; i < groups; ++i) {
             const int buf = i & 1;
-            if (!__all_sync(0xffffffffu, wait_or_flag(S.abort_flag, &S.acc_full[buf], (uint32_t)(i >> 1) & 1, p.ctrl,
-                                                      kDetWaitFull | 0x73)))
+            const uint32_t par = (uint32_t)(i >> 1) & 1;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&S.acc_full[buf], par) ||
+                                             wait_or_flag(S.abort_flag, &S.acc_full[buf], par, p.ctrl, kDetWaitFull | 0x73)))
                 break;
             fence_after();
             const uint32_t tl = tmem + buf * p.nt + half * cols + ((uint32_t)(32 * q) << 16);
 #pragma unroll
-            for (int c = 0; c < 128; c += 16) {
+            for (int c = 0; c < kFewTok / 2; c += 16) {
                 if (c < cols) {
                     uint32_t v[16];
                     tmem_ld16(tl + c, v);
@@ -406,20 +461,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this CTA's sums, [token][plane row] fp32 over the stages' memory
     float* sums = reinterpret_cast<float*>(smem);
     const bool ok = !ld_volatile(S.abort_flag);
-    if (ok && warp >= 4) {
-        float* dst = sums + (size_t)((warp - 4) >> 2) * cols * 128 + 32 * (warp & 3) + lane;
+    if (ok && warp >= kAddWarp0) {
+        float* dst = sums + (size_t)((warp - kAddWarp0) >> 2) * cols * 128 + 32 * (warp & 3) + lane;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
+        for (int c = 0; c < kFewTok / 2; ++c)
             if (c < cols) dst[c * 128] = acc[c];
     }
     fence_before();
     __syncthreads();
     cluster_sync();
     fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) tmem_dealloc(tmem, 256);
     if (ok) {
         const uint32_t sbase = smem_u32(sums);
-        for (int i = part * kThreads + threadIdx.x; i < ntok * (kExp / 4); i += p.split * kThreads) {
+        for (int i = part * kFewThreads + threadIdx.x; i < ntok * (kExp / 4); i += p.split * kFewThreads) {
             const int tok = i / (kExp / 4), c = 4 * (i % (kExp / 4)), e = e0 + c;
             if (e >= p.E) continue;
             const uint32_t at = sbase + (uint32_t)(tok * 128 + c) * 4;
@@ -454,12 +509,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 cudaError_t launch_few(const FewArgs& p, const CUtensorMap& xm, const CUtensorMap& wm, int ttiles, cudaStream_t s) {
-    constexpr size_t smem = 226 * 1024;                   // 512 columns: the whole SM
+    const size_t smem = kFewStages * (kPlanesBytes + (size_t)p.nt * kBK * 2 + kRowsBytes) + 1024;   // > half an SM
     const cudaError_t err = set_smem_limit(scored_logits_few_kernel, smem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.split * ttiles * p.etiles));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -476,7 +531,53 @@ cudaError_t launch_few(const FewArgs& p, const CUtensorMap& xm, const CUtensorMa
 
 }  // namespace
 
-cudaError_t launch_scored_logits(const RouteArgs& a, int num_ctas, cudaStream_t s) {
+LogitPlan plan_scored_logits(const RouteArgs& a, int num_ctas) {
+    // The kernel, its tile and K split with the least estimated time, in clocks: a stage of a pair
+    // 800 and 3 an expert of the tile, one of a single CTA 960; a wave of clusters some 4000 beside
+    // its stages, joining parts 2500, for the single CTAs 16 a token of the tile, and 6000 for the
+    // kernel that writes the pairs' planes.  (Full-size layer, whole call, tiles of 64, 128 and 256
+    // experts: 1024 tokens 44.8, 40.8 and 48.8 us, 3000 tokens 106, 75.6 and 63.2 us.)
+    LogitPlan best = {};
+    const int ptt = (a.T + kTok - 1) / kTok, chunks = a.H / kBK;
+    double clocks = 0.0;
+    for (int cut = 1; cut <= 4; cut *= 2) {
+        const int en = ((a.E + cut - 1) / cut + 63) / 64 * 64;
+        const int64_t tiles = (int64_t)ptt * ((a.E + en - 1) / en);
+        const double stage = 800.0 + 3.0 * en;
+        for (int parts = 1; parts <= 4 && parts <= chunks; ++parts) {
+            const int cap = cluster_capacity(2 * parts, 1, num_ctas);
+            const double waves = (double)((tiles + cap - 1) / cap);
+            const double t =
+                6000.0 + waves * ((chunks + parts - 1) / parts * stage + 4000.0) + (parts > 1 ? 2500.0 : 0.0);
+            if (clocks == 0.0 || t < clocks) {
+                clocks = t;
+                best = {false, parts, en, ptt};
+            }
+        }
+    }
+    const int ttiles = (a.T + kFewTok - 1) / kFewTok, nt = ((a.T + ttiles - 1) / ttiles + 31) / 32 * 32;
+    const int64_t tiles = (int64_t)ttiles * ((a.E + kExp - 1) / kExp);
+    for (int split = 1; split <= kFewSplit && split <= chunks; ++split) {
+        const int cap = cluster_capacity(split, 1, num_ctas);
+        const double waves = (tiles + cap - 1) / cap;
+        const double t = waves * ((chunks + split - 1) / split * 960.0 + 4000.0 + 16.0 * nt) + (split > 1 ? 2500.0 : 0.0);
+        if (t < clocks) {
+            clocks = t;
+            best = {true, split, nt, ttiles};
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_scored_logits(const RouteArgs& a, const LogitPlan& plan, int32_t* sums, int n_sums, cudaStream_t s) {
+    CUtensorMap xm, wm;
+    if (plan.few) {
+        const FewArgs f = {a.T,      a.H,    a.E,  (a.E + kExp - 1) / kExp, plan.nt, plan.parts, a.bias, a.logits,
+                           a.hist,   sums,   (a.T + kChunk - 1) / kChunk * a.E, n_sums, a.ctrl};
+        if (!make_map(&xm, false, a.x, a.T, a.H, a.H, plan.nt) || !make_map_f32(&wm, a.Wr, a.E, a.H, a.H, kExp))
+            return cudaErrorInvalidConfiguration;
+        return launch_few(f, xm, wm, plan.ttiles, s);
+    }
     LogitArgs p = {};
     p.T = a.T;
     p.H = a.H;
@@ -484,51 +585,17 @@ cudaError_t launch_scored_logits(const RouteArgs& a, int num_ctas, cudaStream_t 
     p.bias = a.bias;
     p.logits = a.logits;
     p.ctrl = a.ctrl;
-    const int ttiles = (a.T + kTok - 1) / kTok, chunks = a.H / kBK;
-    // The kernel and K split with the least estimated time, in clocks: 1536 a stage of a pair
-    // or 512 of a single CTA; a wave of clusters some 4000 beside its stages, joining parts
-    // 2500, and for the single CTAs 16 a token of the tile.  (1024 tokens of the full-size
-    // layer, whole call: 46.6 us by pairs, 44.0 us by single CTAs; 4096 tokens: the same.)
-    const int ftt = (a.T + 255) / 256, fnt = ((a.T + ftt - 1) / ftt + 31) / 32 * 32, fet = (a.E + kExp - 1) / kExp;
-    double best = 0.0, few_best = 0.0;
-    int few_split = 1;
-    p.en = (a.E + 63) / 64 * 64;
-    for (int parts = 1; parts <= 4 && parts <= chunks; ++parts) {
-        const int cap = cluster_capacity(2 * parts, 1, num_ctas);
-        const double waves = (ttiles + cap - 1) / cap;
-        const double t = waves * ((chunks + parts - 1) / parts * 1536.0 + 4000.0) + (parts > 1 ? 2500.0 : 0.0);
-        if (best == 0.0 || t < best) {
-            best = t;
-            p.parts = parts;
-        }
-    }
-    for (int split = 1; split <= kFewSplit && split <= chunks; ++split) {
-        const int cap = cluster_capacity(split, 1, num_ctas);
-        const double waves = ((int64_t)ftt * fet + cap - 1) / cap;
-        const double t = waves * ((chunks + split - 1) / split * 512.0 + 4000.0 + 16.0 * fnt) + (split > 1 ? 2500.0 : 0.0);
-        if (few_best == 0.0 || t < few_best) {
-            few_best = t;
-            few_split = split;
-        }
-    }
-    CUtensorMap xm, wm;
-    if (few_best < best) {
-        FewArgs f = {a.T, a.H, a.E, fet, fnt, few_split, 0, a.bias, a.logits, a.ctrl};
-        f.stages = (int)((225 * 1024) / (kPlanesBytes + fnt * kBK * 2));
-        if (f.stages > kMaxStages) f.stages = kMaxStages;
-        if (!make_map(&xm, false, a.x, a.T, a.H, a.H, fnt) ||
-            !make_map(&wm, false, a.planes, 3 * (int64_t)a.E, a.H, a.H, kExp))
-            return cudaErrorInvalidConfiguration;
-        return launch_few(f, xm, wm, ftt, s);
-    }
+    const int ttiles = plan.ttiles;
+    p.parts = plan.parts;
+    p.en = plan.nt;
     p.etiles = (a.E + p.en - 1) / p.en;
     p.tmem_cols = 2 * p.en <= 128 ? 128 : 2 * p.en <= 256 ? 256 : 512;
     const size_t stage = 128 * kBK * 2 + (size_t)3 * (p.en / 2) * kBK * 2;
     p.stages = (int)((226 * 1024 - 1024) / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     size_t smem = p.stages * stage;
-    const size_t sums = (size_t)128 * (p.en + 4) * 4;
-    if (smem < sums) smem = sums;
+    const size_t joined = (size_t)128 * (p.en + 4) * 4;
+    if (smem < joined) smem = joined;
     if (smem < tmem_smem(p.tmem_cols)) smem = tmem_smem(p.tmem_cols);
     smem += 1024;
     if (smem > 226 * 1024) smem = 226 * 1024;             // 512 columns: the whole SM
