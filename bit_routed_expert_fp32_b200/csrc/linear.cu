@@ -213,10 +213,9 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     const uint32_t tmem = S.tmem;
 
     if (warp == 0) {
-        int issued = 0;
+        int issued = 0, s = 0;
+        uint32_t par = 1;
         for (int i = 0; i < n_stage; ++i) {
-            const int s = i % p.stages;
-            const uint32_t par = ((uint32_t)(i / p.stages) & 1) ^ 1;
             if (!mbar_try_wait(&S.empty_[s], par)) wait_or_flag(S.abort_flag, &S.empty_[s], par, p.ctrl, kDetWaitEmpty | 0x60);
             __syncwarp();
             if (ld_volatile(S.abort_flag)) break;
@@ -229,6 +228,10 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
             }
             __syncwarp();
             issued = i + 1;
+            if (++s == p.stages) {
+                s = 0;
+                par ^= 1;
+            }
         }
         // after an abort no copy may still target shared memory: wait (bounded) for the last
         // phase issued on every slot
@@ -254,10 +257,11 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
             }
             __syncwarp();
         }
+        bool ready = false;
+        int s = 0;
+        uint32_t par = 0;
         for (int i = 0; i < n_stage && ok; ++i) {
-            const int s = i % p.stages;
-            const uint32_t par = (uint32_t)(i / p.stages) & 1;
-            if (!mbar_try_wait(&S.full[s], par)) ok = wait_or_flag(S.abort_flag, &S.full[s], par, p.ctrl, kDetWaitFull | 0x60);
+            if (!ready && !mbar_try_wait(&S.full[s], par)) ok = wait_or_flag(S.abort_flag, &S.full[s], par, p.ctrl, kDetWaitFull | 0x60);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             if (ok && elect_one()) {
@@ -269,6 +273,11 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
                 umma_commit(&S.empty_[s]);
             }
             __syncwarp();
+            if (++s == p.stages) {
+                s = 0;
+                par ^= 1;
+            }
+            if (i + 1 < n_stage) ready = mbar_try_wait(&S.full[s], par);
         }
         if (elect_one()) umma_commit(&S.done);          // every MMA issued has completed
         __syncwarp();
