@@ -149,11 +149,12 @@ inline bool vec4_ok(const void* base, int64_t ld, int size) {
     return ld % 4 == 0 && reinterpret_cast<uintptr_t>(base) % (4 * size) == 0;
 }
 
-// The activation of a thread's 8 x 4 values, the choice outside the loops.
-__device__ inline void apply_act_all(int act, float (&o)[8][4]) {
+// The activation of a thread's R x 4 values, the choice outside the loops.
+template <int R>
+__device__ inline void apply_act_all(int act, float (&o)[R][4]) {
 #define MOE_ACT_LOOP(A)                                                                      \
     case A:                                                                                  \
-        _Pragma("unroll") for (int i = 0; i < 8; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j) \
+        _Pragma("unroll") for (int i = 0; i < R; ++i) _Pragma("unroll") for (int j = 0; j < 4; ++j) \
             o[i][j] = apply_act(A, o[i][j]);                                                 \
         break;
     switch (act) {
@@ -172,6 +173,72 @@ struct LinShared {
     uint32_t tmem;
     int abort_flag;
 };
+
+// The outputs of a tile from the parts' sums: a thread forms four columns of every (split *
+// kPer)th token.  All that depends on the columns is outside the loop, and up to how many parts
+// there are (P) is known to the compiler: with two warps a scheduler the loop takes what its
+// instructions and branches take (130 tokens 2048 -> 4096, the kernel without it 5.9 us: with the
+// column's work in the loop 9.6 us, so 8.5; 2048 -> 2 x 4096 with P fixed at eight 13.5 us, so 12.7).
+template <bool F16, bool GLU, int P>
+__device__ inline void linear_outputs(const LinKernelArgs& p, const float* sums, int part, int t0, int ntok, int f0) {
+    constexpr int kOut = GLU ? kFeat / 2 : kFeat, kPer = kLinThreads / (kOut / 4);
+    const int f = 4 * (threadIdx.x % (kOut / 4)), n = f0 + f;
+    if (n >= p.N) return;
+    const bool full = n + 3 < p.N, vec_res = p.vec_res && full, vec = p.vec && full;
+    uint32_t at[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q)
+        if (q < p.split) at[q] = map_peer(smem_u32(sums) + f * 4, q);
+    float bias[4] = {0.f, 0.f, 0.f, 0.f}, bias_up[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias) {
+        const uint16_t* b = static_cast<const uint16_t*>(p.bias) + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) {
+                bias[j] = to_f32<F16>(__ldg(b + j));
+                if (GLU) bias_up[j] = to_f32<F16>(__ldg(b + p.N + j));
+            }
+    }
+    // four sums from every part, in part order
+    auto total = [&](uint32_t off, const float(&b)[4], float(&a)[4]) {
+        float4 v[P];
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            if (q < p.split) v[q] = ld_peer_v4(at[q] + off);
+        a[0] = v[0].x;
+        a[1] = v[0].y;
+        a[2] = v[0].z;
+        a[3] = v[0].w;
+#pragma unroll
+        for (int q = 1; q < P; ++q)
+            if (q < p.split) {
+                a[0] += v[q].x;
+                a[1] += v[q].y;
+                a[2] += v[q].z;
+                a[3] += v[q].w;
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a[j] += b[j];
+    };
+    const int tok0 = part * kPer + threadIdx.x / (kOut / 4), step = p.split * kPer;
+    uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)(t0 + tok0) * p.ldy + n;
+    int64_t ri = (int64_t)(t0 + tok0) * p.ldr + n;
+    for (int tok = tok0; tok < ntok; tok += step, y += step * p.ldy, ri += step * p.ldr) {
+        float res[4] = {0.f, 0.f, 0.f, 0.f}, o[1][4], u[4];
+        if (p.res) load_res4<F16>(p.res, p.res_f32, vec_res, ri, p.N - n, res);
+        total(tok * kFeat * 4, bias, o[0]);
+        if (GLU) {
+            total((tok * kFeat + kOut) * 4, bias_up, u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[0][j] = silu_fast(o[0][j]) * u[j];
+        } else {
+            apply_act_all(p.act, o);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[0][j] += res[j];
+        store4<F16>(y, vec, p.N - n, o[0]);
+    }
+}
 
 template <bool F16, bool GLU>
 __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_constant__ LinKernelArgs p,
@@ -327,52 +394,10 @@ __global__ void __launch_bounds__(kLinThreads, 2) linear_kernel(const __grid_con
     fence_after();
     if (warp == 1) tmem_dealloc(tmem, p.tmem_cols);
     if (ok) {
-        const uint32_t sbase = smem_u32(sums);
-        // four sums from every part, in part order
-        auto total = [&](int row, float(&a)[4]) {
-            const uint32_t at = sbase + (uint32_t)row * 4;
-            float4 v[kMaxSplit];
-#pragma unroll
-            for (int q = 0; q < kMaxSplit; ++q)
-                if (q < p.split) v[q] = ld_peer_v4(map_peer(at, q));
-            a[0] = v[0].x;
-            a[1] = v[0].y;
-            a[2] = v[0].z;
-            a[3] = v[0].w;
-#pragma unroll
-            for (int q = 1; q < kMaxSplit; ++q)
-                if (q < p.split) {
-                    a[0] += v[q].x;
-                    a[1] += v[q].y;
-                    a[2] += v[q].z;
-                    a[3] += v[q].w;
-                }
-        };
-        for (int i = part * kLinThreads + threadIdx.x; i < ntok * (kOut / 4); i += p.split * kLinThreads) {
-            const int tok = i / (kOut / 4), f = 4 * (i % (kOut / 4)), n = f0 + f;
-            if (n >= p.N) continue;
-            const int64_t t = t0 + tok;
-            float o[4], res[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool full = n + 3 < p.N;
-            if (p.res) load_res4<F16>(p.res, p.res_f32, p.vec_res && full, t * p.ldr + n, p.N - n, res);
-            float a[4], u[4];
-            total(tok * kFeat + f, a);
-            if (GLU) total(tok * kFeat + kOut + f, u);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float v = a[j];
-                if (p.bias && n + j < p.N) v += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + n + j));
-                if (GLU) {
-                    if (p.bias && n + j < p.N)
-                        u[j] += to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + p.N + n + j));
-                    v = silu_fast(v) * u[j];
-                } else {
-                    v = apply_act(p.act, v);
-                }
-                o[j] = v + res[j];
-            }
-            store4<F16>(static_cast<uint16_t*>(p.y) + t * p.ldy + n, p.vec && full, p.N - n, o);
-        }
+        if (p.split == 1) linear_outputs<F16, GLU, 1>(p, sums, part, t0, ntok, f0);
+        else if (p.split == 2) linear_outputs<F16, GLU, 2>(p, sums, part, t0, ntok, f0);
+        else if (p.split <= 4) linear_outputs<F16, GLU, 4>(p, sums, part, t0, ntok, f0);
+        else linear_outputs<F16, GLU, kMaxSplit>(p, sums, part, t0, ntok, f0);
     }
     // no CTA's shared memory goes away while another reads it
     __syncwarp();
@@ -416,15 +441,15 @@ TilePlan plan_tiles(const LinearArgs& a) {
         per_sm = per_sm < 1 ? 1 : per_sm > 2 ? 2 : per_sm;
         // The stages' bytes come at the 64 a clock that L2 gives an SM, if there are enough of them
         // in flight for some 2400 clocks; the sums of a token of the tile take some 45 clocks; a
-        // wave some 10600 beside that (launch, first load, barriers).  (One token, 2048 -> 7168:
-        // 13.1 us with one part, 9.9 with two, 9.0 with four or five, 9.2 with six, 12.5 with
-        // eight, in a second wave; 384 tokens, 4096 -> 4096: 23.3 us with two, 32.5 with three,
-        // whose 96 clusters do not fit at once.)
+        // wave some 7000 beside that (launch, first load, barriers).  (16 tokens, 2048 -> 7168:
+        // 11.4 us with one part, 8.0 with two, 7.7 with three, 7.3 with four, 11.8 with six, in a
+        // second wave; 384 tokens, 4096 -> 4096: 20.6 us with two, 28.9 with three, whose 96
+        // clusters do not fit at once.)
         const int64_t cap = (int64_t)cluster_capacity(split, per_sm, a.num_ctas);
         const int64_t waves = (tiles + cap - 1) / cap, ctas = tiles * split;
         const int64_t share = ctas <= a.num_ctas ? 1 : per_sm;
         const double flight = (double)share * p.stages * stage_bytes / 2400.0, rate = flight < 64.0 ? flight : 64.0;
-        p.clocks = (double)waves * (share * per * (stage_bytes / rate) + 10600.0 + 45.0 * p.nt);
+        p.clocks = (double)waves * (share * per * (stage_bytes / rate) + 7000.0 + 45.0 * p.nt);
         // more parts where it makes no difference: less is left to each CTA's first load
         if (best.split == 0 || p.clocks <= 1.02 * best.clocks) best = p;
     }
@@ -1031,20 +1056,22 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     const bool glu = a.act == MOE_ACT_SWIGLU;
     // The vector kernel saves the tile kernel's fixed steps; its loads come nearer to HBM's rate
     // the fewer tokens share the registers.  Measured (vector against tile kernel, us): one
-    // token 2 MB of weights 2.1 / 4.1, 17 MB 4.8 / 7.1, 29 MB 7.9 / 9.4, 59 MB 11.3 / 12.7, 76 MB
-    // 17.0 / 15.7, 134 MB 26.1 / 23.7; four tokens 2 MB 3.2 / 4.2, 8 MB 5.5 / 6.1, 17 MB 7.7 / 7.5.
+    // token 2 MB of weights 2.2 / 4.1, 17 MB 3.8 / 6.4, 29 MB 6.7 / 7.9, 59 MB 10.9 / 12.7, 73 MB
+    // 16.7 / 14.7; four tokens 2 MB 3.2 / 4.2, 8 MB 4.6 / 5.5, 17 MB 6.4 / 6.7, 29 MB 10.7 / 8.0.
     const int64_t bytes = (int64_t)2 * a.K * a.N * (glu ? 2 : 1);
-    if (bytes <= (a.T == 1 ? (int64_t)64 << 20 : a.T <= kVecTok ? (int64_t)12 << 20 : 0)) {
+    if (bytes <= (a.T == 1 ? (int64_t)64 << 20 : a.T <= kVecTok ? (int64_t)20 << 20 : 0)) {
         if (glu) return a.f16 ? launch_vec_n<true, true>(a, s) : launch_vec_n<false, true>(a, s);
         return a.f16 ? launch_vec_n<true, false>(a, s) : launch_vec_n<false, false>(a, s);
     }
     // A pair's stage takes its MMAs (512 clocks, 545 measured), a wave of pairs some 13000 beside
-    // its tiles.  (4096 -> 4096, tile against pair kernel, us: 130 tokens 14.6 / 25.2, 256 16.8 /
-    // 25.4, 512 24.0 / 24.8, 768 40.5 / 27.3; 512 -> 8192: 130 tokens 11.7 / 9.8.)
+    // its tiles, the last wave's activation 4000 that the tile kernel's smaller tiles do not see.
+    // (2048 -> 4096, tile against pair kernel, us: 130 tokens 8.5 / 14.9, 512 14.2 / 15.5, 768
+    // 20.3 / 16.6; 512 -> 4096: 512 tokens 9.3 / 8.3, with silu 9.8 / 10.5.)
     const TilePlan pl = plan_tiles(a);
     const int64_t ptiles = (int64_t)((a.T - 1) / kPairTok + 1) * ((a.N - 1) / (glu ? 128 : 256) + 1);
     const int64_t waves = (ptiles + a.num_ctas / 2 - 1) / (a.num_ctas / 2);
-    if (13000.0 + (double)waves * ((a.K + kBK - 1) / kBK) * 545.0 < pl.clocks) {
+    const double base = a.act == MOE_ACT_NONE ? 13000.0 : 17000.0;
+    if (base + (double)waves * ((a.K + kBK - 1) / kBK) * 545.0 < pl.clocks) {
         if (glu) return a.f16 ? launch_pair<true, true>(a, s) : launch_pair<false, true>(a, s);
         return a.f16 ? launch_pair<true, false>(a, s) : launch_pair<false, false>(a, s);
     }
