@@ -309,10 +309,20 @@ def moe_route_fixed(cfg, T, x, ids, gates, rt: dict, ws, stream=None) -> None:
 
 def moe_route_scored(cfg, router: Router, T, x, router_w, router_b, balance, rt: dict, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a balance bias (device float32 [E] or None)
-    that steers the choice only, expert groups and scaled weights.  Runs on `stream` (default:
-    the current stream of x's device)."""
+    that steers the choice only, expert groups and scaled weights.  x: bfloat16, T or more rows
+    of H; router_w: float32 [E][H].  Runs on `stream` (default: the current stream of x's
+    device)."""
     import torch
     dev = x.get_device()
+    if (dev < 0 or x.dtype is not torch.bfloat16 or not x.is_contiguous() or x.numel() < T * cfg.H
+            or router_w.dtype is not torch.float32 or not router_w.is_contiguous() or router_w.get_device() != dev
+            or router_w.numel() != cfg.E * cfg.H or ws.get_device() != dev):
+        raise ValueError("moe_route_scored: x must be contiguous bfloat16 [T][H], router_w contiguous float32 [E][H], "
+                         "and x, router_w and ws on one CUDA device")
+    for v in (router_b, balance):
+        if v is not None and (v.dtype is not torch.float32 or v.get_device() != dev or v.numel() != cfg.E
+                              or not v.is_contiguous()):
+            raise ValueError("moe_route_scored: router_b and balance must be contiguous float32 [E] on x's device")
     args = (ctypes.byref(Shape(cfg.H, cfg.I, cfg.E, cfg.k, cfg.S)), ctypes.byref(router), T, x.data_ptr(),
             router_w.data_ptr(), None if router_b is None else router_b.data_ptr(),
             None if balance is None else balance.data_ptr(), ctypes.byref(routing_struct(rt)), ws.data_ptr(),

@@ -34,7 +34,7 @@ int cluster_capacity(int size, int per_sm, int num_ctas) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (set_smem_limit(capacity_kernel, smem) != cudaSuccess ||
+    if (set_smem_limit(capacity_kernel, kMaxDynSmem) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, capacity_kernel, &cfg) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = guess > 0 ? guess : 1;

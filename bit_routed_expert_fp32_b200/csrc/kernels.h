@@ -241,7 +241,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
 // Raises a kernel's dynamic shared memory limit on the current device.  The attribute
 // belongs to the device's context, so it is set before every launch rather than once
 // per process: a host-side call that enqueues nothing, cheap, and correct whichever
-// device is current and from any number of host threads.
+// device is current and from any number of host threads (a kernel whose size varies from call
+// to call is given kMaxDynSmem: a thread must not lower the limit that another launches under).
+constexpr size_t kMaxDynSmem = 226 * 1024;
 template <typename... KArgs>
 inline cudaError_t set_smem_limit(void (*kern)(KArgs...), size_t bytes) {
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

@@ -484,7 +484,7 @@ cudaError_t launch(const LinearArgs& a, const TilePlan& pl, cudaStream_t s) {
     if (!make_map(&wm, F16, a.w, (int64_t)(GLU ? 2 : 1) * a.N, a.K, a.ldw, kOut) ||
         !make_map(&xm, F16, a.x, a.T, a.K, a.ldx, p.nt))
         return cudaErrorInvalidConfiguration;
-    cudaError_t err = set_smem_limit(linear_kernel<F16, GLU>, pl.smem);
+    cudaError_t err = set_smem_limit(linear_kernel<F16, GLU>, kMaxDynSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);

@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     }
     griddep_wait();
     if (warp == 1) tmem_alloc(&S.tmem, 256);
-    for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_hist; i += gridDim.x * kFewThreads) p.hist[i] = 0;
-    for (int i = blockIdx.x * kFewThreads + threadIdx.x; i < p.n_sums; i += gridDim.x * kFewThreads) p.sums[i] = 0;
+    const int64_t id0 = (int64_t)blockIdx.x * kFewThreads + threadIdx.x, ids = (int64_t)gridDim.x * kFewThreads;
+    for (int64_t i = id0; i < p.n_hist; i += ids) p.hist[i] = 0;
+    for (int64_t i = id0; i < p.n_sums; i += ids) p.sums[i] = 0;
     fence_before();
     __syncthreads();
     fence_after();
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
 cudaError_t launch_few(const FewArgs& p, const CUtensorMap& xm, const CUtensorMap& wm, int ttiles, cudaStream_t s) {
     const size_t smem = kFewStages * (kPlanesBytes + (size_t)p.nt * kBK * 2 + kRowsBytes) + 1024;   // > half an SM
-    const cudaError_t err = set_smem_limit(scored_logits_few_kernel, smem);
+    const cudaError_t err = set_smem_limit(scored_logits_few_kernel, kMaxDynSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.split * ttiles * p.etiles));
@@ -591,17 +592,17 @@ cudaError_t launch_scored_logits(const RouteArgs& a, const LogitPlan& plan, int3
     p.etiles = (a.E + p.en - 1) / p.en;
     p.tmem_cols = 2 * p.en <= 128 ? 128 : 2 * p.en <= 256 ? 256 : 512;
     const size_t stage = 128 * kBK * 2 + (size_t)3 * (p.en / 2) * kBK * 2;
-    p.stages = (int)((226 * 1024 - 1024) / stage);
+    p.stages = (int)((kMaxDynSmem - 1024) / stage);
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     size_t smem = p.stages * stage;
     const size_t joined = (size_t)128 * (p.en + 4) * 4;
     if (smem < joined) smem = joined;
     if (smem < tmem_smem(p.tmem_cols)) smem = tmem_smem(p.tmem_cols);
     smem += 1024;
-    if (smem > 226 * 1024) smem = 226 * 1024;             // 512 columns: the whole SM
+    if (smem > kMaxDynSmem) smem = kMaxDynSmem;           // 512 columns: the whole SM
     if (!make_map(&xm, false, a.x, a.T, a.H, a.H, 128) || !make_map(&wm, false, a.planes, 3 * (int64_t)a.E, a.H, a.H, p.en / 2))
         return cudaErrorInvalidConfiguration;
-    cudaError_t err = set_smem_limit(scored_logits_kernel, smem);
+    cudaError_t err = set_smem_limit(scored_logits_kernel, kMaxDynSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * p.parts * ttiles * p.etiles));

@@ -275,3 +275,71 @@ def test_on_a_stream_that_is_not_the_tensors_own():
     moe.moe_linear(x, w, y, ws, act=moe.ACT_SILU, stream=s)
     s.synchronize()
     check_linear(y, x, w, None, None, moe.ACT_SILU)
+
+
+def test_host_threads_calling_at_once():
+    """Calls whose kernels ask for different amounts of shared memory, from two host threads."""
+    import threading
+    import torch
+    import bit_routed_expert_fp32_b200 as moe
+    K, N, E = 512, 384, 48
+    w = (torch.randn(N, K, device="cuda") / K ** 0.5).to(torch.bfloat16)
+    wr = torch.randn(E, K, device="cuda") * 0.02
+    cfg = SimpleNamespace(H=K, I=64, E=E, k=4, S=0)
+    torch.cuda.synchronize()
+    got, failed = {}, []
+
+    def work(me, sizes):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                jobs = []
+                for T in sizes:
+                    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+                    ws = torch.empty(moe.moe_workspace_size(cfg, T), dtype=torch.uint8, device="cuda")
+                    moe.moe_workspace_init(ws)
+                    jobs.append((T, x, torch.empty(T, N, dtype=torch.bfloat16, device="cuda"), ws, moe.alloc_routing(cfg, T)))
+                for _ in range(200):
+                    for T, x, y, ws, rt in jobs:
+                        moe.moe_linear(x, w, y, ws)
+                        moe.moe_route_scored(cfg, moe.Router(), T, x, wr, None, None, rt, ws)
+                s.synchronize()
+                got[me] = jobs
+        except Exception as e:                                # noqa: BLE001 - shown by the assert below
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i, sizes)) for i, sizes in enumerate([(12, 140, 700), (40, 90, 2000)])]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for jobs in got.values():
+        for T, x, y, ws, rt in jobs:
+            y2, rt2 = torch.empty_like(y), moe.alloc_routing(cfg, T)
+            assert moe.moe_get_error(ws) == (0, 0)
+            moe.moe_linear(x, w, y2, ws)
+            moe.moe_route_scored(cfg, moe.Router(), T, x, wr, None, None, rt2, ws)
+            torch.cuda.synchronize()
+            assert torch.equal(y, y2) and all(torch.equal(rt[n], rt2[n]) for n in rt)
+
+
+def test_the_router_binding_refuses_tensors_that_do_not_fit():
+    import torch
+    import bit_routed_expert_fp32_b200 as moe
+    cfg = SimpleNamespace(H=128, I=64, E=16, k=2, S=0)
+    ws = torch.empty(moe.moe_workspace_size(cfg, 8), dtype=torch.uint8, device="cuda")
+    moe.moe_workspace_init(ws)
+    rt = moe.alloc_routing(cfg, 8)
+    x = torch.zeros((8, 128), dtype=torch.bfloat16, device="cuda")
+    w, b = torch.zeros((16, 128), device="cuda"), torch.zeros(16, device="cuda")
+    for kw in (dict(x=x.half()), dict(x=x.cpu()), dict(x=x[:7]), dict(x=x[:, :64]), dict(w=w.double()), dict(w=w.cpu()),
+               dict(w=w[:15]), dict(w=w.t()), dict(b=b[:15]), dict(b=b.double()), dict(bal=b.cpu()),
+               dict(bal=torch.zeros(32, device="cuda")[::2]), dict(ws=ws.cpu())):
+        a = dict(x=x, w=w, b=b, bal=b, ws=ws)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            moe.moe_route_scored(cfg, moe.Router(), 8, a["x"], a["w"], a["b"], a["bal"], rt, a["ws"])
+    moe.moe_route_scored(cfg, moe.Router(), 8, x, w, b, b, rt, ws)
+    torch.cuda.synchronize()
+    assert rt["topk_ids"].tolist() == [[0, 1]] * 8 and moe.moe_get_error(ws) == (0, 0)

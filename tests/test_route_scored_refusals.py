@@ -33,3 +33,15 @@ def test_workspace_and_empty_batch():
     assert call(ws_bytes=4096) == 3
     assert call(T=0) == 0
     assert call(T=0, G=3) == 1
+
+
+def test_tensors_are_checked_before_their_pointers_are_used():
+    """Host tensors, other types and too few rows are refused by the Python entry."""
+    torch = pytest.importorskip("torch")
+
+    class Cfg:
+        H, I, E, k, S = 128, 64, 16, 2, 0
+    x, w = torch.zeros((4, 128), dtype=torch.bfloat16), torch.zeros((16, 128))
+    ws = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA device"):
+        moe.moe_route_scored(Cfg, moe.Router(), 4, x, w, None, None, {}, ws)
