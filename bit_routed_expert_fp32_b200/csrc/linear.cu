@@ -691,32 +691,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             pair_tile(p, tile, tt, ft);
             const int buf = n & 1;
             const int t0 = tt * kPairTok + rank * 128 + 32 * q, nb = ft * kOut + half * kCols;
-            // whole columns in aligned rows move four values at a time; rows past the last token
-            // read its residual and are not written
+            // whole columns in aligned rows move four values at a time; otherwise a lane keeps to one
+            // column, so that the single values of a row still move together.  Rows past the last
+            // token (and columns past the last) read its residual and are not written.
             const bool whole = t0 < p.T && nb + kCols <= p.N && p.vec && (!p.res || p.vec_res);
             const int left = p.T - t0;
             // without a residual the values are rounded before they change lanes: half the bytes
             const bool packed = whole && p.vec8 && !p.res && (!p.bias || p.vec_bias);
             uint4 rbuf[8];
             auto load_res = [&](int c0) {
-                const int n = nb + c0 + 4 * c4;
-                const int64_t at = (int64_t)t0 * p.ldr + n;
-                if (!whole) {
-                    // odd strides, or the last columns: value by value, as fp32 (columns past the
-                    // last read the last one's)
+                const int64_t at = (int64_t)t0 * p.ldr + nb + c0 + 4 * c4;
+                if (!whole) {                              // row 4 i + j in piece j of rbuf[i], res16 as it is
+                    const int64_t col = (int64_t)t0 * p.ldr + min(nb + c0 + lane, p.N - 1);
+                    auto rows = [&](auto* src) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int64_t ri = at + min(4 * i + lr, left - 1) * p.ldr;
-                        float f[4];
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t f[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int64_t k = ri + min(j, p.N - 1 - n);
-                            f[j] = res16 ? to_f32<F16>(static_cast<const uint16_t*>(p.res)[k])
-                                         : static_cast<const float*>(p.res)[k];
+                            for (int j = 0; j < 4; ++j) f[j] = src[min(4 * i + j, left - 1) * p.ldr];
+                            rbuf[i] = make_uint4(f[0], f[1], f[2], f[3]);
                         }
-                        rbuf[i] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                                             __float_as_uint(f[3]));
-                    }
+                    };
+                    if (res16) rows(static_cast<const uint16_t*>(p.res) + col);
+                    else rows(static_cast<const uint32_t*>(p.res) + col);
                 } else if (res16) {
                     const uint16_t* src = static_cast<const uint16_t*>(p.res) + at;
 #pragma unroll
@@ -810,20 +807,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                     __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
                 __syncwarp();
                 float o[8][4];
+                if (whole) {                               // o[i][j]: row 4 i + lr, column 4 c4 + j
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + lr;
-                    const float4 f = sq[r * 8 + (c4 ^ (r & 7))];
-                    o[i][0] = f.x;
-                    o[i][1] = f.y;
-                    o[i][2] = f.z;
-                    o[i][3] = f.w;
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + lr;
+                        const float4 f = sq[r * 8 + (c4 ^ (r & 7))];
+                        o[i][0] = f.x;
+                        o[i][1] = f.y;
+                        o[i][2] = f.z;
+                        o[i][3] = f.w;
+                    }
+                } else {                                   // o[i][j]: row 4 i + j, column lane
+                    const float* sf = reinterpret_cast<const float*>(sq) + (lane & 3);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 4 * i + j;
+                            o[i][j] = sf[4 * (r * 8 + ((lane >> 2) ^ (r & 7)))];
+                        }
                 }
                 if (!GLU) {
                     if (p.bias) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const float b = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + min(nc + j, p.N - 1)));
+                            const int col = min(whole ? nc + j : n0 + lane, p.N - 1);
+                            const float b = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + col));
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i][j] += b;
                         }
@@ -832,25 +841,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 }
                 uint16_t* yp = static_cast<uint16_t*>(p.y) + (int64_t)(t0 + lr) * p.ldy + nc;
                 if (p.res && left > 0) {
+                    if (!res16) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (res16 && whole) {
-                            o[i][0] += to_f32<F16>(rbuf[i].x & 0xFFFF);
-                            o[i][1] += to_f32<F16>(rbuf[i].x >> 16);
-                            o[i][2] += to_f32<F16>(rbuf[i].y & 0xFFFF);
-                            o[i][3] += to_f32<F16>(rbuf[i].y >> 16);
-                        } else {
+                        for (int i = 0; i < 8; ++i) {
                             o[i][0] += __uint_as_float(rbuf[i].x);
                             o[i][1] += __uint_as_float(rbuf[i].y);
                             o[i][2] += __uint_as_float(rbuf[i].z);
                             o[i][3] += __uint_as_float(rbuf[i].w);
                         }
+                    } else if (whole) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            o[i][0] += to_f32<F16>(rbuf[i].x & 0xFFFF);
+                            o[i][1] += to_f32<F16>(rbuf[i].x >> 16);
+                            o[i][2] += to_f32<F16>(rbuf[i].y & 0xFFFF);
+                            o[i][3] += to_f32<F16>(rbuf[i].y >> 16);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            o[i][0] += to_f32<F16>(rbuf[i].x);
+                            o[i][1] += to_f32<F16>(rbuf[i].y);
+                            o[i][2] += to_f32<F16>(rbuf[i].z);
+                            o[i][3] += to_f32<F16>(rbuf[i].w);
+                        }
                     }
                     if (c0 + 32 < kCols) load_res(c0 + 32);
                 }
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (4 * i + lr < left && nc < p.N) store4<F16>(yp + 4 * i * p.ldy, whole, p.N - nc, o[i]);
+                    for (int i = 0; i < 8; ++i)
+                        if (4 * i + lr < left) store4<F16>(yp + 4 * i * p.ldy, true, 4, o[i]);
+                } else if (n0 + lane < p.N) {
+                    uint16_t* yc = static_cast<uint16_t*>(p.y) + (int64_t)t0 * p.ldy + n0 + lane;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j, yc += p.ldy)
+                            if (4 * i + j < left) *yc = (uint16_t)from_f32<F16>(o[i][j]);
+                }
             }
             fence_before();
             __syncwarp();
