@@ -129,14 +129,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         int slot = 0;
         uint32_t par = 0;
-        bool ready = false;
         for (int i = 0; i < n_stage && ok; ++i) {
             const int g = i / kDrain, buf = g & 1;
             const bool first = i % kDrain == 0, last = i % kDrain == kDrain - 1 || i == n_stage - 1;
-            if (!ready)
-                ok = (!first || pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
-                                          kDetWaitEmpty | 0x71)) &&
-                     pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x70);
+            ok = (!first || pair_wait(S.abort_flag, &S.acc_empty[buf], (uint32_t)((g >> 1) & 1) ^ 1, p.ctrl,
+                                      kDetWaitEmpty | 0x71)) &&
+                 pair_wait(S.abort_flag, &S.full[slot], par, p.ctrl, kDetWaitFull | 0x70);
             ok = __all_sync(0xffffffffu, ok);
             fence_after();
             if (ok && elect_one()) {
@@ -155,10 +153,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 slot = 0;
                 par ^= 1;
             }
-            // a wait is some 130 clocks of this warp's time: the next stage's are begun together
-            if (i + 1 == n_stage) break;
-            ready = mbar_try_wait(&S.full[slot], par);
-            if (last) ready &= mbar_try_wait(&S.acc_empty[buf ^ 1], (uint32_t)(((g + 1) >> 1) & 1) ^ 1);
         }
         if (!ok) {                                        // what was issued ends before either CTA leaves
             if (elect_one()) umma_commit_pair(&S.drained, pair_mask);
@@ -387,7 +381,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 slot = 0;
                 par ^= 1;
             }
-            if (i + 1 == n_stage) break;                  // the next stage's waits, as above
+            // a wait is some 130 clocks of this warp's time: the next stage's are begun together
+            if (i + 1 == n_stage) break;
             ready = mbar_try_wait(&S.split[slot], par);
             if (last) ready &= mbar_try_wait(&S.acc_empty[buf ^ 1], (uint32_t)(((g + 1) >> 1) & 1) ^ 1);
         }
