@@ -398,9 +398,8 @@ __device__ inline void load_balance(const ScoreArgs& r, int E, int lane, float (
 // its rows, 32 contiguous bytes, as the fragments of two MMAs.  A warp's sum is short (its
 // few steps, the small pieces in an accumulator of their own); warps and CTAs are added in
 // double-float.  Up to 8 tokens the last CTA to finish (a ticket) chooses, a warp per token,
-// and permutes, while the others form the decode operands; above, one CTA of 32 warps does
-// that in a kernel of its own (16 tokens: 17.7 us with a last CTA of 16 warps, 17.3 us with
-// the two kernels of larger counts, 13.1 us with one).
+// and permutes, while the others form the decode operands; above, a kernel of its own does that
+// (16 tokens: 17.7 us with a last CTA of 16 warps, 12.7 us so).
 constexpr int kSmExperts = 16, kSmStep = 32, kSmParts = 8, kTailT = 8;
 
 template <int NTL, int NW>   // 8-token MMA columns, warps
@@ -576,28 +575,33 @@ __global__ void __launch_bounds__(32 * NW, 2)
     cluster_wait();
 }
 
-// The choice and the permutation of up to kSmallT tokens: one CTA, a warp per token at a time;
-// then eight warps rank a contiguous share of the pairs each.  The other CTAs form the decode
-// operands of (token, group) pairs meanwhile, one per warp.
+// The choice and the permutation of up to kSmallT tokens: a cluster of eight CTAs takes a
+// contiguous part of the tokens each, a warp per token, counts its experts in shared memory,
+// forms its bases from the others' counts, and permutes.  The other clusters form the decode
+// operands of (token, group) pairs meanwhile, one per warp.  (Whole call, one CTA of 32 warps,
+// whose choice its SM's instruction rate bounds, against the cluster: full-size layer 16 tokens
+// 13.3 / 12.7 us, 32 16.9 / 14.8, 64 25.8 / 18.8; H 2048, 64 experts 8.7 / 9.0, 10.9 / 9.4,
+// 15.6 / 10.9.)
+constexpr int kChooseCtas = 8, kChooseWarps = kSmallT / kChooseCtas;
 struct ChooseSmem {
     union {
-        Scratch scratch[32];
-        int run[8][256];
+        Scratch scratch[kChooseWarps];
+        int run[kChooseWarps][256];
     };
-    int32_t ids[kSmallT * 16];
-    int cnt[256];
+    int32_t ids[kChooseWarps * 16];
+    int cnt[256], total[256], base[256];
     int off[257];
 };
 
-__global__ void __launch_bounds__(1024) scored_choose_kernel(RouteArgs p, ScoreArgs r) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    ChooseSmem& S = *reinterpret_cast<ChooseSmem*>(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = p.T * p.k;
-    if (threadIdx.x < 256) S.cnt[threadIdx.x] = 0;
+__global__ void __launch_bounds__(32 * kChooseWarps) scored_choose_kernel(RouteArgs p, ScoreArgs r) {
+    static_assert(32 * kChooseWarps == 256, "a thread per expert");
+    __shared__ ChooseSmem S;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
+    S.cnt[e] = 0;
     griddep_launch_dependents();
     griddep_wait();
-    if (blockIdx.x > 0) {
-        const int G8 = 8 * ((p.H / 64 + 7) / 8), pr = (int)(blockIdx.x - 1) * 32 + warp;
+    if (blockIdx.x >= kChooseCtas) {
+        const int G8 = 8 * ((p.H / 64 + 7) / 8), pr = (int)(blockIdx.x - kChooseCtas) * kChooseWarps + warp;
         if (pr < p.T * G8) {
             const OperandArgs o{p.T, p.H, p.x, p.zx, p.iq, p.ctrl};
             compute_z(o, pr / G8, pr % G8, lane);
@@ -605,41 +609,62 @@ __global__ void __launch_bounds__(1024) scored_choose_kernel(RouteArgs p, ScoreA
         }
         return;
     }
+    const int rank = (int)cluster_rank(), per = (p.T + kChooseCtas - 1) / kChooseCtas;
+    const int t0 = min(p.T, rank * per), t1 = min(p.T, t0 + per), n = (t1 - t0) * p.k, t = t0 + warp;
     float bal[8];
     load_balance(r, p.E, lane, bal);
     __syncthreads();
-    for (int t = warp; t < p.T; t += 32) {
+    if (t < t1) {
+        int32_t* ids = S.ids + warp * p.k;
         select_scored(r, p.E, p.k, p.logits + (size_t)t * p.E, bal, S.scratch[warp], lane, p.r.topk_ids + (size_t)t * p.k,
-                      p.r.topk_w + (size_t)t * p.k, S.ids + t * p.k);
+                      p.r.topk_w + (size_t)t * p.k, ids);
         __syncwarp();
-        if (lane < p.k) atomicAdd(&S.cnt[S.ids[t * p.k + lane]], 1);
+        if (lane < p.k) atomicAdd(&S.cnt[ids[lane]], 1);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 8 * 256; i += 1024) S.run[i >> 8][i & 255] = 0;
-    __syncthreads();
-    const int share = (n + 255) / 256 * 32, b0 = min(n, warp * share), b1 = min(n, b0 + share);
-    if (warp < 8)
-        for (int i = b0 + lane; i < b1; i += 32) atomicAdd(&S.run[warp][S.ids[i]], 1);
-    else if (warp == 8)
-        warp_scan_counts(S.cnt, S.off, p.E, lane);
-    else if (warp == 9)
-        warp_active(S.cnt, p.E, p.S, p.active, p.ctrl, p.T, lane);
-    __syncthreads();
-    const int e = threadIdx.x;
-    if (e < p.E) {
-        int run = S.off[e];
-        p.r.counts[e] = S.cnt[e];
-        p.r.offsets[e] = run;
+    __syncwarp();
+    cluster_sync();                     // every CTA's counts are there; scratch is free
+    {
+        const uint32_t at = smem_u32(&S.cnt[e]);
+        int c[kChooseCtas], base = 0, total = 0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
+        for (int q = 0; q < kChooseCtas; ++q)
+            asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[q]) : "r"(map_peer(at, q)) : "memory");
+#pragma unroll
+        for (int q = 0; q < kChooseCtas; ++q) {
+            base += q < rank ? c[q] : 0;
+            total += c[q];
+        }
+        S.base[e] = base;
+        S.total[e] = total;
+#pragma unroll
+        for (int w = 0; w < kChooseWarps; ++w) S.run[w][e] = 0;
+    }
+    cluster_arrive();                   // this CTA has read the others' counts
+    __syncthreads();
+    // each warp counts and then ranks 32 of the pairs (8 x 16 at most: four warps)
+    const int b0 = min(n, warp * 32), b1 = min(n, b0 + 32);
+    if (b0 + lane < b1) atomicAdd(&S.run[warp][S.ids[b0 + lane]], 1);
+    if (warp == kChooseWarps - 1) warp_scan_counts(S.total, S.off, p.E, lane);
+    if (warp == kChooseWarps - 2 && rank == 0) warp_active(S.total, p.E, p.S, p.active, p.ctrl, p.T, lane);
+    __syncthreads();
+    if (e < p.E) {
+        int run = S.off[e] + S.base[e];
+        if (rank == 0) {
+            p.r.counts[e] = S.total[e];
+            p.r.offsets[e] = S.off[e];
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
             const int v = S.run[w][e];
             S.run[w][e] = run;
             run += v;
         }
     }
-    if (e == 0) p.r.offsets[p.E] = S.off[p.E];
+    if (e == 0 && rank == 0) p.r.offsets[p.E] = S.off[p.E];
     __syncthreads();
-    if (warp < 8) warp_scatter(S.ids + b0, b0, b1 - b0, S.run[warp], p.r.perm, p.r.inv_perm, lane, p.E);
+    if (b0 < b1) warp_scatter(S.ids + b0, t0 * p.k + b0, b1 - b0, S.run[warp], p.r.perm, p.r.inv_perm, lane, p.E);
+    __syncwarp();
+    cluster_wait();                     // a CTA leaves only when its counts have been read
 }
 
 // ---------------------------------------------------------------- above kSmallT tokens
@@ -780,10 +805,22 @@ cudaError_t launch_route_scored(const RouteArgs& a, const ScoreArgs& r, int num_
     if (a.T <= kSmallT) {
         if (a.T <= kTailT) return launch_small<1, 8>(a, r, s);
         err = a.T <= 16 ? launch_small<2, 8>(a, r, s) : a.T <= 32 ? launch_small<4, 8>(a, r, s) : launch_small<8, 8>(a, r, s);
-        if (err == cudaSuccess) err = set_smem_limit(scored_choose_kernel, sizeof(ChooseSmem));
         if (err != cudaSuccess) return err;
-        const int pairs = a.ops ? a.T * 8 * ((a.H / 64 + 7) / 8) : 0;
-        return launch_pdl(scored_choose_kernel, dim3(1 + (pairs + 31) / 32), dim3(1024), sizeof(ChooseSmem), s, a, r);
+        const int pairs = a.ops ? a.T * 8 * ((a.H / 64 + 7) / 8) : 0, ctas = (pairs + kChooseWarps - 1) / kChooseWarps;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((1 + (ctas + kChooseCtas - 1) / kChooseCtas) * kChooseCtas);
+        cfg.blockDim = dim3(32 * kChooseWarps);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kChooseCtas;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, scored_choose_kernel, a, r);
     }
     // the spans' sums and the planes take regions of the workspace that only moe_forward uses
     const int nchunks = (a.T + kChunk - 1) / kChunk, n_sums = (nchunks + kSpan - 1) / kSpan * a.E;
