@@ -181,13 +181,19 @@ __device__ inline void bulk_g2s(void* dst_smem, const void* src_gmem, uint32_t b
         : "memory");
 }
 
-// Programmatic dependent launch.  A kernel launched with programmatic stream
-// serialization may start before its predecessor in the stream has finished: it must
-// call griddep_wait() before it reads anything the predecessor writes (or overwrites
-// anything the predecessor reads).  griddep_launch_dependents() lets the next kernel's
-// launch begin; kernels call it only when all of their CTAs are resident at once, so
-// the successor's CTAs never take an SM that one of their own still needs.  Both are
-// no-ops for kernels launched without the attribute.
+// Programmatic dependent launch.  A kernel launched with programmatic stream serialization
+// may start before its predecessor in the stream has finished; griddep_wait() returns once the
+// predecessor, and so everything that it waited for itself, is complete and visible.
+// griddep_launch_dependents() lets the next kernel start: when every CTA of the grid has
+// started and called it (or exited), so a successor never takes an SM that a CTA of this grid
+// still needs.  Both are no-ops for kernels launched without the attribute.  The rules:
+// - Before its wait a kernel writes nothing and reads only what no kernel still running can be
+//   writing: the packed experts, and (ffn_decode_kernel) the token rows that the router read.
+// - That holds only if nothing older than the predecessor still runs.  So the kernels that may
+//   follow another call's (of moe_linear and moe_route_scored: all of them) release their
+//   dependents after their own wait, or (the first kernels of moe_forward) the call ends with a
+//   kernel that releases none early.  A release before the wait would let the decode pass start,
+//   and pull token rows into L1, while the product two launches before it still writes them.
 __device__ inline void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ inline void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 

@@ -582,9 +582,11 @@ __device__ __forceinline__ void unit_epilogue(const FfnArgs& p, const Geo& geo, 
 }
 
 // Gate/up with few tokens: every SM reads the same token rows and Z values, so each CTA
-// pulls them into L1 at the start.  The token rows are the caller's input (ready before
-// the router ran); the Z values are the router's output and are prefetched only after
-// griddep_wait(), so no stale line can enter L1.  The zx region is padded to 256 bytes,
+// pulls them into L1 at the start.  The token rows are the caller's input, complete before this
+// kernel can start: the router read them, and a router's kernel releases its dependents only
+// after its own wait for whatever wrote them (moe_route's kernels are ordinary launches).  The Z
+// values are the router's output and are prefetched only after griddep_wait().  So no stale line
+// can enter L1.  The zx region is padded to 256 bytes,
 // so whole lines stay inside it.
 __device__ inline size_t z_bytes(const FfnArgs& p) { return (size_t)3 * p.T * (8 * ((p.H / 64 + 7) / 8)) * 4; }
 __device__ inline bool warm_fits(const FfnArgs& p) { return (size_t)p.T * p.H * 2 + z_bytes(p) <= 48 * 1024; }

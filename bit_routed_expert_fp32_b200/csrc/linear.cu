@@ -971,7 +971,6 @@ __global__ void __launch_bounds__(32 * kVecWarps) linear_vec_kernel(const __grid
     const int groups = kVecWarps / p.parts, grp = warp / p.parts, part = warp - grp * p.parts;
     const int n0 = (blockIdx.x * groups + grp) * kOut;
     const int steps = (p.K + 255) / 256, s0 = part * steps / p.parts, s1 = (part + 1) * steps / p.parts;
-    griddep_launch_dependents();
     const uint16_t* rows[kVecRows];
 #pragma unroll
     for (int r = 0; r < kVecRows; ++r) {
@@ -984,6 +983,7 @@ __global__ void __launch_bounds__(32 * kVecWarps) linear_vec_kernel(const __grid
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[r][t] = 0.f;
     griddep_wait();
+    griddep_launch_dependents();
     auto add = [&](const uint4(&wv)[kVecRows], const uint4(&xv)[NT]) {
         float xf[NT][8];
 #pragma unroll

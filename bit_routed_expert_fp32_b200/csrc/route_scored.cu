@@ -423,7 +423,6 @@ __global__ void __launch_bounds__(32 * NW, 2)
     constexpr bool kTail = 8 * NTL <= kTailT;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SmallSmem<NTL, NW>& S = *reinterpret_cast<SmallSmem<NTL, NW>*>(smem_raw);
-    griddep_launch_dependents();        // one wave of CTAs: the next kernel may start launching
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const int part = (int)cluster_rank(), e0 = (int)(blockIdx.x / parts) * kSmExperts;
     const int steps = p.H / kSmStep;
@@ -435,6 +434,7 @@ __global__ void __launch_bounds__(32 * NW, 2)
     const bool rows[2] = {e0 + g < p.E, e0 + g + 8 < p.E};
     const float* w0 = p.Wr + (size_t)(e0 + g) * p.H + 8 * t4;
     griddep_wait();
+    griddep_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) {              // no expert pass of this workspace runs now
         p.ctrl->work[0] = 0;
         p.ctrl->work[1] = 0;
@@ -598,8 +598,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) scored_choose_kernel(RouteA
     __shared__ ChooseSmem S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
     S.cnt[e] = 0;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     if (blockIdx.x >= kChooseCtas) {
         const int G8 = 8 * ((p.H / 64 + 7) / 8), pr = (int)(blockIdx.x - kChooseCtas) * kChooseWarps + warp;
         if (pr < p.T * G8) {
@@ -672,8 +672,8 @@ __global__ void __launch_bounds__(32 * kChooseWarps) scored_choose_kernel(RouteA
 // upper bits of what is left), for the logits kernel's operand loads; zeroes the histograms
 // that the top-k kernel adds to.
 __global__ void __launch_bounds__(256) scored_split_kernel(RouteArgs p, uint16_t* planes, int32_t* sums, int n_sums) {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const size_t n8 = (size_t)p.E * p.H / 8, plane = (size_t)p.E * p.H;
     const size_t i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x, step = (size_t)gridDim.x * blockDim.x;
     for (size_t i = i0; i < (size_t)n_sums; i += step) sums[i] = 0;
@@ -700,8 +700,8 @@ constexpr int kTopWarps = 4, kSpan = 16;
 
 __global__ void __launch_bounds__(32 * kTopWarps, 6) scored_topk_kernel(RouteArgs p, ScoreArgs r, int32_t* sums) {
     __shared__ Scratch s_scratch[kTopWarps];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = blockIdx.x * kTopWarps + warp, c = t / kChunk;
     if (t >= p.T) return;
@@ -724,8 +724,8 @@ __global__ void __launch_bounds__(256) scored_scatter_kernel(RouteArgs p, const 
     __shared__ int s_cnt[256];
     __shared__ int s_off[257];
     __shared__ int s_run[8][256];
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = threadIdx.x;
     const int c = blockIdx.x, span = c / kSpan, n_spans = ((int)gridDim.x + kSpan - 1) / kSpan;
     int base = 0, total = 0;
