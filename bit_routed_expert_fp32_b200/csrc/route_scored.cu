@@ -7,6 +7,8 @@
 // The logits are fp32 as in moe_route; scores and choice are formed from them in fp64: the
 // sigmoid's upper end leaves fp32 scores equal whose logits differ, and a sum of score and
 // bias loses what separates two of them.
+#include <float.h>
+
 #include "operands.cuh"
 #include "route_common.cuh"
 #include "tc5.cuh"
@@ -182,12 +184,13 @@ __device__ inline float unkey32(uint32_t k) { return __uint_as_float((k & 0x8000
 // documented error of 2 + 1.17 |x| ulp counts in proportion to s (1 - s): 8e-8 at most), one
 // rounding and the fast quotient (two ulp) are off by at most 2.7e-7; softmax scores by at
 // most 2.6e-6 of the largest (ten ulp of the sum's terms on average, its thirteen additions,
-// the terms' own few ulp).  Adding the balance rounds once more.  So where neighbours among the k + 1 largest
-// values (and the group scores beside the border) lie further apart than both can be off,
-// their order is the exact one; otherwise, and where NaN or infinities meet, false is
-// returned and the careful path decides.  A softmax without balance has the order of its
-// logits (as long as fp64 scores would not vanish).  A key gives its low three bits to the
-// expert's place in the lane; a lane's eight are sorted once and then only popped.
+// the terms' own few ulp).  Adding the balance rounds once more, relative to the value
+// it gives.  So where neighbours among the k + 1 largest values (and the scores of the kept
+// groups and of the others) lie further apart than both can be off, their order is the exact
+// one; otherwise, and where NaN or infinities meet, false is returned and the careful path
+// decides.  A softmax without balance has the order of its logits (as long as fp64 scores would
+// not vanish).  A key gives its low three bits to the expert's place in the lane; a lane's eight
+// are sorted once and then only popped.
 __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, const float (&L)[8], const float (&b)[8],
                                             Scratch& scratch, int lane, int& my_id) {
     // what two scores can be off together, and, relative to their sum of sizes, what the
@@ -267,21 +270,28 @@ __device__ __forceinline__ bool choose_fast(const ScoreArgs& r, int E, int k, co
             leader = 1;
         }
         // the best groups one by one; lanes past the last group hold none
-        const float sc = r.group_top == 2 ? t1 + t2 : t1;
-        uint32_t rest = lane < r.n_groups * leader ? key32(sc) : 0u, lo = 0;
-        if (__any_sync(0xffffffffu, rest != 0 && sc != sc)) return false;
+        const bool pair = r.group_top == 2, group = lane < r.n_groups * leader;
+        const float sc = pair ? t1 + t2 : t1;
+        uint32_t rest = group ? key32(sc) : 0u;
+        if (__any_sync(0xffffffffu, group && sc != sc)) return false;
         unsigned lanes = 0;
         for (int n = 0; n < r.top_groups; ++n) {
-            lo = __reduce_max_sync(0xffffffffu, rest);
-            const bool hit = rest == lo;
+            const uint32_t top = __reduce_max_sync(0xffffffffu, rest);
+            const bool hit = rest == top;
             lanes |= __ballot_sync(0xffffffffu, hit);
             if (hit) rest = 0;
         }
-        const float flo = unkey32(lo), fhi = unkey32(__reduce_max_sync(0xffffffffu, rest));
-        // groups that tie, and infinities, are left to fp64
-        if (__popc(lanes) != r.top_groups * leader ||
-            !(flo - fhi > 2.f * abs_err + kRel * (fabsf(flo) + fabsf(fhi))))
-            return false;
+        // What a group's score can be off goes with its terms: a sum that cancels keeps what
+        // rounding them has lost.  (An infinite term makes the sum exact; a finite sum past the
+        // type's range counts as its end.)  No kept group may reach down to what another can reach.
+        const bool exact = fabsf(t1) == INFINITY || (pair && fabsf(t2) == INFINITY);
+        const float mid = exact ? sc : fminf(fmaxf(sc, -FLT_MAX), FLT_MAX);
+        const float off = exact ? 0.f : abs_err + kRel * fabsf(t1) + (pair ? kRel * fabsf(t2) : 0.f);
+        const bool kept = (lanes >> lane) & 1u;
+        const uint32_t lo = __reduce_min_sync(0xffffffffu, kept ? key32(mid - off) : 0xffffffffu);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, group && !kept ? key32(mid + off) : 0u);
+        // groups that tie, and infinities that meet, are left to fp64
+        if (__popc(lanes) != r.top_groups * leader || lo <= hi) return false;
         if (leader > 1 || gs == 8) {                       // a lane's experts are of one group
             if (!((lanes >> lane) & 1u))
 #pragma unroll
