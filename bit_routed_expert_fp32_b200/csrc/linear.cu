@@ -73,9 +73,17 @@ __device__ inline uint32_t pack2(float lo, float hi) {
     return r;
 }
 
-// silu with the fast exponential and quotient: relative error about 1e-6, far below the
-// 16-bit rounding of the output
-__device__ inline float silu_fast(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+// a / (1 + e^-z) = a (2^-15 / (2^-15 + 2^(-z log2 e - 15))): so scaled, the divisor leaves the range
+// of the approximate reciprocal only below z = -97, where a times it is less than half of bf16's
+// smallest value (unscaled from -87 on, where SiLU is still 1e-36).  The relative error, some 2^-22
+// and 2^-23 |z|, is far below the output's rounding.
+__device__ inline float sigmoid_times(float a, float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(z, -1.44269504f, -15.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0x1p-15f));
+    return a * (r * 0x1p-15f);
+}
+__device__ inline float silu_fast(float a) { return sigmoid_times(a, a); }
 
 __device__ inline float apply_act(int act, float a) {
     switch (act) {
@@ -99,8 +107,7 @@ __device__ inline float apply_act(int act, float a) {
         }
         case MOE_ACT_GELU_TANH: {
             // (1 + tanh z) / 2 = 1 / (1 + e^-2z)
-            const float z2 = 1.59576912f * (a + 0.044715f * a * a * a);
-            return __fdividef(a, 1.f + __expf(-z2));
+            return sigmoid_times(a, 1.59576912f * (a + 0.044715f * a * a * a));
         }
     }
     return a;

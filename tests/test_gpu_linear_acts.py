@@ -3,12 +3,14 @@ argument itself (K = 1), so that the fp32 sum is exact and only the activation a
 of its result are off.
 
 Tolerance: half a step of the type, and what the fp32 formulas may lose, in steps of 2^-23 of the
-value, z being the argument of the exponential: the fast exponential's documented 2 + 1.17 z, the
-fast quotient's 2, and
-  SiLU       the sum 1 + t and the product a t: 1 each                               6 + 1.2 z
-  tanh GELU  the same; z itself (seven roundings of half a step, times z): 4 z       6 + 5.2 z
+value, z being the argument of the exponential:
+  SiLU       2^(-z log2 e - 15): the argument's rounding, half a step of 1.45 z + 15, 5.2 + 0.5 z,
+             log2 e itself 0.25 z, ex2.approx 2; the sum 0.5, rcp.approx 1, the product 0.5
+                                                                                     10 + 0.8 z
+  tanh GELU  the same; z itself (seven roundings of half a step, times z): 4 z       10 + 4.8 z
   GELU       erfc's fit 5.4, its seven terms with alternating signs (the largest is 0.4, their sum
-             down to 0.06) 6, z = a a / 2: z                                         16 + 2.5 z
+             down to 0.06) and the quotient 8, z = a a / 2: z, the exponential 2 + 1.17 z
+                                                                                     16 + 2.5 z
 and half of the smallest subnormal, which in fp32 loses bits too below 2^-126: 2^-149 (1 + |a|)."""
 import pytest
 
@@ -68,7 +70,7 @@ def one(act, dtype, T, copies):
     assert moe.moe_get_error(ws) == (0, 0)
     assert torch.equal(y, y[:1].expand(T, N))
     ref, z = definition(act, a)
-    c0, c1 = {moe.ACT_SILU: (6, 1.2), moe.ACT_SWIGLU: (6, 1.2), moe.ACT_GELU_TANH: (6, 5.2), moe.ACT_GELU: (16, 2.5)}[act]
+    c0, c1 = {moe.ACT_SILU: (10, 0.8), moe.ACT_SWIGLU: (10, 0.8), moe.ACT_GELU_TANH: (10, 4.8), moe.ACT_GELU: (16, 2.5)}[act]
     fi = torch.finfo(dt)
     tol = (fi.eps / 2 + (c0 + c1 * z.clamp_max(120)) * 2.0 ** -23) * ref.abs()
     tol = tol + fi.smallest_normal * fi.eps / 2 + 2.0 ** -149 * (1 + a.double().abs())
@@ -82,3 +84,12 @@ def one(act, dtype, T, copies):
 @pytest.mark.parametrize("T,copies", KERNELS)
 def test_gelu(T, copies, dtype):
     one(_moe().ACT_GELU, dtype, T, copies)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,copies", KERNELS)
+@pytest.mark.parametrize("act", ["SILU", "SWIGLU", "GELU_TANH"])
+def test_sigmoid_forms(act, T, copies, dtype):
+    """Down to where fp32 ends: bf16 holds SiLU's values far past -87, where 1 + e^-a leaves the
+    range of the fast quotient's divisor."""
+    one(getattr(_moe(), "ACT_" + act), dtype, T, copies)
