@@ -310,8 +310,8 @@ def moe_route_fixed(cfg, T, x, ids, gates, rt: dict, ws, stream=None) -> None:
 def moe_route_scored(cfg, router: Router, T, x, router_w, router_b, balance, rt: dict, ws, stream=None) -> None:
     """moe_route with softmax or sigmoid scores, a balance bias (device float32 [E] or None)
     that steers the choice only, expert groups and scaled weights.  x: bfloat16, T or more rows
-    of H; router_w: float32 [E][H].  Runs on `stream` (default: the current stream of x's
-    device)."""
+    of H; router_w: float32 [E][H]; rt: alloc_routing's buffers for T or more tokens.  Runs on
+    `stream` (default: the current stream of x's device)."""
     import torch
     dev = x.get_device()
     if (dev < 0 or x.dtype is not torch.bfloat16 or not x.is_contiguous() or x.numel() < T * cfg.H
@@ -323,6 +323,13 @@ def moe_route_scored(cfg, router: Router, T, x, router_w, router_b, balance, rt:
         if v is not None and (v.dtype is not torch.float32 or v.get_device() != dev or v.numel() != cfg.E
                               or not v.is_contiguous()):
             raise ValueError("moe_route_scored: router_b and balance must be contiguous float32 [E] on x's device")
+    i32, n = torch.int32, T * cfg.k
+    for name, dt, size in (("topk_ids", i32, n), ("topk_w", torch.float32, n), ("counts", i32, cfg.E),
+                           ("offsets", i32, cfg.E + 1), ("perm", i32, n), ("inv_perm", i32, n)):
+        v = rt[name]
+        if v.dtype is not dt or v.numel() < size or v.get_device() != dev or not v.is_contiguous():
+            raise ValueError(f"moe_route_scored: rt[{name!r}] must be contiguous {dt} of {size} or more elements on x's "
+                             "device")
     args = (ctypes.byref(Shape(cfg.H, cfg.I, cfg.E, cfg.k, cfg.S)), ctypes.byref(router), T, x.data_ptr(),
             router_w.data_ptr(), None if router_b is None else router_b.data_ptr(),
             None if balance is None else balance.data_ptr(), ctypes.byref(routing_struct(rt)), ws.data_ptr(),
