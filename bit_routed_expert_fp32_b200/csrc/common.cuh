@@ -194,6 +194,8 @@ __device__ inline void bulk_g2s(void* dst_smem, const void* src_gmem, uint32_t b
 //   dependents after their own wait, or (the first kernels of moe_forward) the call ends with a
 //   kernel that releases none early.  A release before the wait would let the decode pass start,
 //   and pull token rows into L1, while the product two launches before it still writes them.
+// - What a predecessor may have written is read by plain loads, which stay behind the wait; the
+//   non-coherent ones (__ldg) are for data that is constant from the kernel's start on.
 __device__ inline void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ inline void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 

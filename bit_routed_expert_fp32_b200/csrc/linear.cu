@@ -208,8 +208,8 @@ __device__ inline void linear_outputs(const LinKernelArgs& p, const float* sums,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (n + j < p.N) {
-                bias[j] = to_f32<F16>(__ldg(b + j));
-                if (GLU) bias_up[j] = to_f32<F16>(__ldg(b + p.N + j));
+                bias[j] = to_f32<F16>(b[j]);
+                if (GLU) bias_up[j] = to_f32<F16>(b[p.N + j]);
             }
     }
     // four sums from every part, in part order
@@ -765,8 +765,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (n0 + j < p.N) {
-                                v[j] = __float_as_uint(__uint_as_float(v[j]) + to_f32<F16>(__ldg(bp + j)));
-                                u[j] = __float_as_uint(__uint_as_float(u[j]) + to_f32<F16>(__ldg(bp + p.N + j)));
+                                v[j] = __float_as_uint(__uint_as_float(v[j]) + to_f32<F16>(bp[j]));
+                                u[j] = __float_as_uint(__uint_as_float(u[j]) + to_f32<F16>(bp[p.N + j]));
                             }
                     }
 #pragma unroll
@@ -779,7 +779,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 float b[8];
-                                unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n0) + j), b);
+                                unpack8<F16>(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.bias) + n0)[j], b);
 #pragma unroll
                                 for (int u = 0; u < 8; ++u)
                                     v[8 * j + u] = __float_as_uint(__uint_as_float(v[8 * j + u]) + b[u]);
@@ -845,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int col = min(whole ? nc + j : n0 + lane, p.N - 1);
-                            const float b = to_f32<F16>(__ldg(static_cast<const uint16_t*>(p.bias) + col));
+                            const float b = to_f32<F16>(static_cast<const uint16_t*>(p.bias)[col]);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) o[i][j] += b;
                         }
@@ -957,17 +957,18 @@ struct VecArgs {
     uint16_t* y;
 };
 
-// 16 bytes that are read once (they stay out of L1).
+// 16 bytes that are read once (they stay out of L1).  Not through the non-coherent path, which is
+// for what nothing writes while the kernel runs: this one may start while an input is written.
 __device__ inline uint4 ld_stream(const void* p) {
     uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                  : "l"(p));
     return r;
 }
 // Eight elements at k of a row of K, zero past its end.
 __device__ inline uint4 load8(const uint16_t* row, int k, int K) {
-    if (k + 8 <= K) return __ldg(reinterpret_cast<const uint4*>(row + k));
+    if (k + 8 <= K) return *reinterpret_cast<const uint4*>(row + k);
     uint32_t u[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -1025,7 +1026,7 @@ __global__ void __launch_bounds__(32 * kVecWarps) linear_vec_kernel(const __grid
 #pragma unroll
             for (int r = 0; r < kVecRows; ++r) wv[u][r] = ld_stream(rows[r] + k);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) xv[u][t] = __ldg(reinterpret_cast<const uint4*>(xr[t] + k));
+            for (int t = 0; t < NT; ++t) xv[u][t] = *reinterpret_cast<const uint4*>(xr[t] + k);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) add(wv[u], xv[u]);
@@ -1061,8 +1062,8 @@ __global__ void __launch_bounds__(32 * kVecWarps) linear_vec_kernel(const __grid
         if (GLU) b += s_sum[g * p.parts + q][kOut + r][t];
     }
     if (p.bias) {
-        a += to_f32<F16>(__ldg(p.bias + n));
-        if (GLU) b += to_f32<F16>(__ldg(p.bias + p.N + n));
+        a += to_f32<F16>(p.bias[n]);
+        if (GLU) b += to_f32<F16>(p.bias[p.N + n]);
     }
     float v = GLU ? silu_fast(a) * b : apply_act(p.act, a);
     if (p.res) {

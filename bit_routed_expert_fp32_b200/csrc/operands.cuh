@@ -42,7 +42,7 @@ __device__ inline void compute_z(const OperandArgs& p, int t, int Gi, int lane) 
     const int G = p.H / 64, G8 = 8 * ((G + 7) / 8);
     float z[3] = {0.f, 0.f, 0.f};
     if (Gi < G) {
-        const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p.x + (size_t)t * p.H + Gi * 64) + lane);
+        const uint32_t v = reinterpret_cast<const uint32_t*>(p.x + (size_t)t * p.H + Gi * 64)[lane];
         const float x0 = op_bf16lo(v), x1 = op_bf16hi(v);
         // tokens outside the fp16 range (or not finite) are outside what the expert
         // kernels compute: reported, not carried on (see moe_forward)
@@ -112,7 +112,7 @@ __device__ inline void compute_iq(const OperandArgs& p, int t, int Gi, int lane)
         if (lane == 0) pairs[Gi] = make_float2(0.f, 0.f);
         return;
     }
-    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p.x + (size_t)t * p.H + Gi * 64) + lane);
+    const uint32_t v = reinterpret_cast<const uint32_t*>(p.x + (size_t)t * p.H + Gi * 64)[lane];
     iq_group(op_bf16lo(v), op_bf16hi(v), lane, p.iq + ((size_t)t * G + Gi) * 128, pairs + Gi);
 }
 

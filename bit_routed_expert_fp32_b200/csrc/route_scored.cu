@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(32 * NW, 2)
             for (int n = 0; n < NTL; ++n) {
                 const int t = 8 * n + g;
                 xv[u][n] = in && t < p.T
-                               ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)t * p.H + k0 + 8 * t4))
+                               ? *reinterpret_cast<const uint4*>(p.x + (size_t)t * p.H + k0 + 8 * t4)
                                : make_uint4(0, 0, 0, 0);
             }
         }

@@ -119,3 +119,66 @@ def test_layers_one_after_the_other(T):
     apart, chained = go(True), go(False)
     assert moe.moe_get_error(one.ws) == (0, 0) and moe.moe_get_error(two.ws) == (0, 0)
     assert torch.isfinite(apart).all() and torch.equal(apart, chained)
+
+
+@pytest.mark.parametrize("name,data", [("linear.cu", ""), ("route_scored.cu", "p.x"), ("operands.cuh", "p.x")])
+def test_what_a_product_may_have_written_is_read_coherently(name, data):
+    """The non-coherent loads are for data that is constant from the kernel's start on; a kernel
+    started early may read rows, weights or biases that its predecessor is still writing then."""
+    text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    loads = [m.group(0) for m in re.finditer(r"(__ldg\s*\(|ld\.global\.nc)[^;]*;", text)]
+    assert not [ld for ld in loads if data in ld]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 3, 4, 20, 200, 700])
+def test_every_input_of_a_product_written_by_the_one_before(T):
+    """x, then the weights, the bias and the residual of a product are each the output of the product
+    launched just before it, in buffers that earlier products of the chain have read."""
+    import torch
+    import bit_routed_expert_fp32_b200 as moe
+    K = 256
+    ws = torch.empty(4096, dtype=torch.uint8, device="cuda")
+    moe.moe_workspace_init(ws)
+    g = torch.Generator(device="cuda").manual_seed(T)
+
+    def rnd(*s, std=1.0):
+        return (torch.randn(*s, generator=g, device="cuda") * std).to(torch.bfloat16)
+
+    srcs = [(rnd(T, 4096), rnd(K, 4096, std=1 / 64), rnd(K, 512, std=1 / 20), rnd(K, 512, std=1 / 20), rnd(1, 4096)) for _ in range(6)]
+
+    def go(wait):
+        x, r, y = (torch.zeros(T, K, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+        w, b = torch.zeros(K, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+        outs = []
+
+        def product(a, m, out, **kw):
+            moe.moe_linear(a, m, out, ws, **kw)
+            if wait:
+                torch.cuda.synchronize()
+
+        def use():
+            outs.append(torch.empty_like(y))
+            product(x, w, outs[-1], bias=b[0], residual=r, act=moe.ACT_SILU)
+
+        kept = [torch.empty(T, K, dtype=torch.bfloat16, device="cuda") for _ in range(30)]     # no allocation in between
+        del kept
+        torch.cuda.synchronize()
+        for a, m, w1, w2, v in srcs:
+            product(a, m, x)
+            use()
+            product(w1, w2, w)
+            use()
+            product(v, m, b)
+            use()
+            product(a, m, r, residual=x)
+            use()
+            product(a, m, r, residual=r, act=moe.ACT_RELU)                                    # in place
+            use()
+        torch.cuda.synchronize()
+        return torch.stack(outs)
+
+    apart, chained = go(True), go(False)
+    assert moe.moe_get_error(ws) == (0, 0)
+    assert torch.isfinite(apart).all() and len({o.float().cpu().numpy().tobytes() for o in apart[2:]}) == len(apart) - 2
+    assert torch.equal(apart, chained)
