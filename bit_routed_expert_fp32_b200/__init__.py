@@ -466,7 +466,8 @@ class MoeLayer:
     router, balance: a scored router (moe_route_scored) in place of the softmax top-k.
     shared: (w_gate_up [2 I_s][H], w_down [H][I_s]), bfloat16 device tensors of an expert kept
     at 16 bits that every token uses (moe_linear): y = routed sum + w_down (silu(gate) * up),
-    the routed sum entering in fp32, so that y is rounded once."""
+    the routed sum entering in fp32, so that y is rounded once.  forward's events then lie around
+    the routed experts' kernels, before these two products."""
 
     def __init__(self, cfg, packed_host: np.ndarray, router_w: np.ndarray, router_b, max_tokens: int,
                  device="cuda", router: Router = None, balance=None, shared=None):

@@ -11,6 +11,13 @@
 // part order (no atomics: the result does not depend on timing), and applies the epilogue.
 // Sending the sums to the CTA that adds them, instead of its reading them, measured slower
 // (one token, 2048 -> 7168: 10.4 against 9.0 us): the barrier then waits for remote stores.
+//
+// Sums are fp32 throughout.  The tensor core truncates its running sums instead of rounding them:
+// through K = 7168 a sum comes out 7e-6 of its size too small on average, 1.5 % of half a step of
+// fp16 and 0.2 % of bf16's, as in any 16-bit product on this part (the library's has the same
+// share of outputs that are not the nearest value: fp16 2.8 %, with sums that round 0.6 %).  A fresh
+// accumulator every so often, as the router's logits have it, would cost the pair kernel the
+// epilogue's overlap.
 #include "tc5.cuh"
 
 namespace moe {

@@ -1,5 +1,5 @@
 // tcgen05, tensor-map and cluster wrappers of the kernels whose operands are plain 16-bit
-// matrices (linear.cu, route_scored.cu): both operands from shared memory, K-major rows of
+// matrices (linear.cu, scored_logits.cu): both operands from shared memory, K-major rows of
 // 64 elements in the 128-byte swizzle.
 #pragma once
 #include <cuda.h>
