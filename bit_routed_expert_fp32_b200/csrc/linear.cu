@@ -1105,9 +1105,12 @@ cudaError_t launch_vec_n(const LinearArgs& a, cudaStream_t s) {
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
     const bool glu = a.act == MOE_ACT_SWIGLU;
     // The vector kernel saves the tile kernel's fixed steps; its loads come nearer to HBM's rate
-    // the fewer tokens share the registers.  Measured (vector against tile kernel, us): one
-    // token 2 MB of weights 2.2 / 4.1, 17 MB 3.8 / 6.4, 29 MB 6.7 / 7.9, 59 MB 10.9 / 12.7, 73 MB
-    // 16.7 / 14.7; four tokens 2 MB 3.2 / 4.2, 8 MB 4.6 / 5.5, 17 MB 6.4 / 6.7, 29 MB 10.7 / 8.0.
+    // the fewer tokens share the registers.  Measured (vector against tile kernel, us, weights from
+    // HBM): one token 29 MB 7.9 / 8.8, 34 MB 8.3 / 9.2, 59 MB as 7168 -> 4096 12.2 / 12.9, 73 MB
+    // 18.1 / 15.1, 88 MB 18.9 / 17.5; four tokens 17 MB 7.7 / 6.9 to 7.5, 34 MB 12.1 / 9.4 (from L2,
+    // 2 MB 3.2 / 4.2, 8 MB 4.6 / 5.5).  The limits by bytes are coarse: what costs the vector kernel
+    // is CTAs that do not spread evenly over the SMs (59 MB as 5760 -> 5120, whose 320 CTAs leave
+    // some SMs three and others two: 16.2 / 12.6; as 4608 -> 6400 13.5 / 12.6).
     const int64_t bytes = (int64_t)2 * a.K * a.N * (glu ? 2 : 1);
     if (bytes <= (a.T == 1 ? (int64_t)64 << 20 : a.T <= kVecTok ? (int64_t)20 << 20 : 0)) {
         if (glu) return a.f16 ? launch_vec_n<true, true>(a, s) : launch_vec_n<false, true>(a, s);
