@@ -100,8 +100,8 @@ __device__ inline float apply_act(int act, float a) {
             // a Phi(a), Phi(-|a|) = q = erfc(x) / 2 with x = |a| / sqrt 2, and erfc(x) = e^-x^2 t P(t),
             // t = 1 / (1 + 3/8 x): the form of Abramowitz and Stegun's 7.1.26 with seven terms,
             // fitted for the least relative error up to x = 9.6 (6.4e-7; theirs is small beside 1
-            // only, so that GELU was off by 8e-4 of its value at -4).  A quarter of erfcf's
-            // instructions.
+            // only, 8e-4 of GELU's value at -4).  (GELU prompts take 1 to 5 % longer than with
+            // their five terms: 2048 tokens 2048 -> 4096 31.3 against 30.5 us.)
             const float t = __fdividef(1.f, fmaf(0.26516504f, fabsf(a), 1.f));
             float q = fmaf(-0.1350959f, t, 0.38793784f);
             q = fmaf(q, t, -0.12959732f);
